@@ -9,6 +9,25 @@
 
 namespace dsa {
 
+// Launch as a programmatic dependent of the kernel ahead in the stream: the
+// kernel may start early and waits (grid_dependency_wait) before it reads.
+template <class... KArgs, class... Args>
+inline cudaError_t launch_dependent(void (*kern)(KArgs...), int grid, int block, size_t smem, cudaStream_t st,
+                                    const Args &...args) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(grid);
+    cfg.blockDim = dim3(block);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = st;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    cudaError_t e = cudaLaunchKernelEx(&cfg, kern, args...);
+    return e != cudaSuccess ? e : cudaGetLastError();
+}
+
 // ------------------------------------------------- page tables and slot maps
 constexpr int kTabThreads = 512;
 constexpr int kTabMaxSeq = 16384;  // three int32 per sequence in shared memory: 192 KB
@@ -21,7 +40,7 @@ struct TableParams {
     int32_t vec;         // the token arrays are 16-byte aligned
     int32_t in_place;    // kv_len is seq_len, or free_head_out is free_head
     int64_t n_pages;     // page ids are 0..n_pages-1
-    uint32_t *arrived;   // ws: CTAs that have finished; zero between calls
+    int32_t *taken;      // ws: pages handed out, from k13 to k13_advance (in place)
     int *status;
 };
 cudaError_t launch_build_tables(const TableParams &a, int grid, cudaStream_t st);

@@ -239,7 +239,7 @@ int dsa_table_workspace_size(const dsa_table_params *tp, size_t *bytes) {
     int rc = check_tables(tp);
     if (rc) return rc;
     if (!bytes) return fail(DSA_ERR_INVALID_ARG, "bytes is NULL");
-    *bytes = 512;  // status word; counter of finished CTAs
+    *bytes = 512;  // status word; pages handed out
     return DSA_OK;
 }
 
@@ -286,7 +286,7 @@ int dsa_build_tables(const dsa_table_params *tp, const int32_t *seq_len, const i
     a.in_place = kv_len == seq_len || free_head_out == free_head;
     a.n_pages = tp->cache_rows / tp->page_size;
     a.status = at<int>(ws, 0);
-    a.arrived = at<uint32_t>(ws, 256);
+    a.taken = at<int32_t>(ws, 256);
     // a CTA for every 2048 tokens or 64 sequences, at most one per SM
     const int by_tokens = (tp->nt + 4 * kTabThreads - 1) / (4 * kTabThreads), by_seqs = (tp->nseq + 63) / 64;
     int grid = by_tokens > by_seqs ? by_tokens : by_seqs;

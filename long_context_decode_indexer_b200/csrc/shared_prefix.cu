@@ -896,25 +896,6 @@ __global__ void __launch_bounds__(256) k19_prefix_join(const PrefixParams a) {
     if (lane == 0 && col == 0) a.lse[row] = total == 0.f ? -INFINITY : base + logf(total);
 }
 
-namespace {
-template <class... KArgs, class... Args>
-cudaError_t launch_dependent(void (*kern)(KArgs...), int grid, int block, size_t smem, cudaStream_t st,
-                             const Args &...args) {
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(grid);
-    cfg.blockDim = dim3(block);
-    cfg.dynamicSmemBytes = smem;
-    cfg.stream = st;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    cudaError_t e = cudaLaunchKernelEx(&cfg, kern, args...);
-    return e != cudaSuccess ? e : cudaGetLastError();
-}
-}  // namespace
-
 cudaError_t launch_shared_prefix(const CUtensorMap &qmap, const CUtensorMap &kmap, const CUtensorMap &vmap,
                                  const PrefixParams &a, cudaStream_t st) {
     const size_t plan_bytes = PlanSmem::bytes(a.nq, a.ngroups);

@@ -13,8 +13,10 @@
 // scan), then takes its share of the tokens (each finds its sequence by a
 // binary search in shared memory) and of the sequences (one warp each, for
 // the table entries).  Nothing a CTA reads is written by another.  Where the
-// new lengths or the new head replace the old ones, the last CTA to finish
-// writes them.  What bounds it is the chain of dependent loads: lengths,
+// new lengths or the new head replace the old ones, a small second kernel
+// writes them once every CTA has read the old ones (a counter of finished
+// CTAs would do without it, but would rely on what earlier calls left in the
+// workspace).  What bounds it is the chain of dependent loads: lengths,
 // shared-memory search, page (4.5 us for 128 sequences of two tokens, 10.8 us
 // for 4096 sequences and 100000 tokens).
 #include <cuda_runtime.h>
@@ -57,13 +59,13 @@ __device__ __forceinline__ void copy_entries(int32_t *to, const int32_t *from, i
 
 }  // namespace
 
-__global__ void __launch_bounds__(kTabThreads) k13_build_tables(const TableParams a) {
+__global__ void __launch_bounds__(kTabThreads, 1) k13_build_tables(const TableParams a) {
     extern __shared__ int32_t sm_tab[];
     int32_t *tok0 = sm_tab;                    // [nseq + 1] new_len, then the first token of each sequence
     int32_t *page0 = sm_tab + a.nseq + 1;      // [nseq + 1] pages needed, then the first new page
     int32_t *len = sm_tab + 2 * (a.nseq + 1);  // [nseq] cached positions
     __shared__ uint32_t warp_tok[kTabThreads / 32], warp_page[kTabThreads / 32];
-    __shared__ int bad_any, last;
+    __shared__ int bad_any;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int ps = a.page_size;
     const int head = *a.free_head;
@@ -205,8 +207,10 @@ __global__ void __launch_bounds__(kTabThreads) k13_build_tables(const TableParam
         if (!a.in_place) a.kv_len[b] = refuse ? a.seq_len[b] : len[b] + (tok0[b + 1] - tok0[b]);
     }
     if (gtid == 0) {
+        const int32_t taken = refuse ? 0 : static_cast<int32_t>(total_p);
         a.q_start[a.nseq] = ntok;
-        if (!a.in_place) *a.free_head_out = head + (refuse ? 0 : static_cast<int32_t>(total_p));
+        if (a.in_place) *a.taken = taken;
+        else *a.free_head_out = head + taken;
     }
     if (!refuse)
         for (int b = gtid >> 5; b < a.nseq; b += gthreads >> 5) {
@@ -218,19 +222,15 @@ __global__ void __launch_bounds__(kTabThreads) k13_build_tables(const TableParam
             copy_entries(row + held, a.free_pages + head + page0[b], need, lane,
                          [&](int p) { return p >= 0 && p < a.n_pages ? p : -1; });
         }
-    if (!a.in_place) return;
-    // ---- the last CTA advances the lengths and the head
-    __threadfence();
-    __syncthreads();
-    if (tid == 0) last = atomicAdd(a.arrived, 1u) == gridDim.x - 1;
-    __syncthreads();
-    if (!last) return;
-    for (int b = tid; b < a.nseq; b += kTabThreads)
-        a.kv_len[b] = refuse ? a.seq_len[b] : len[b] + (tok0[b + 1] - tok0[b]);
-    if (tid == 0) {
-        *a.free_head_out = head + (refuse ? 0 : static_cast<int32_t>(total_p));
-        *a.arrived = 0;
-    }
+}
+
+// The lengths and the head in place, after k13: a refused batch has offsets
+// of 0 throughout, so its lengths stay.
+__global__ void __launch_bounds__(kTabThreads) k13_advance(const TableParams a) {
+    grid_dependency_wait();
+    const int b = blockIdx.x * kTabThreads + threadIdx.x;
+    if (b < a.nseq) a.kv_len[b] = a.seq_len[b] + (a.q_start[b + 1] - a.q_start[b]);
+    if (b == 0) *a.free_head_out = *a.free_head + *a.taken;
 }
 
 cudaError_t launch_build_tables(const TableParams &a, int grid, cudaStream_t st) {
@@ -241,7 +241,9 @@ cudaError_t launch_build_tables(const TableParams &a, int grid, cudaStream_t st)
         if (e != cudaSuccess) return e;
     }
     k13_build_tables<<<grid, kTabThreads, smem, st>>>(a);
-    return cudaGetLastError();
+    cudaError_t e = cudaGetLastError();
+    if (e != cudaSuccess || !a.in_place) return e;
+    return launch_dependent(k13_advance, a.nseq > 0 ? (a.nseq + kTabThreads - 1) / kTabThreads : 1, kTabThreads, 0, st, a);
 }
 
 }  // namespace dsa

@@ -232,3 +232,26 @@ def test_calls_on_two_streams():
     torch.cuda.synchronize()
     for s in steps:
         s.check()
+
+
+@pytest.mark.parametrize("alias", ["both", "lengths", "head"])
+@pytest.mark.parametrize("fill", [0xAB, 1])
+def test_in_place_on_a_workspace_that_another_call_wrote(alias, fill):
+    """Only the status word of a workspace has to hold from call to call:
+    lengths and head advance in place whatever the rest of it holds."""
+    rng = np.random.default_rng(8)
+    seq, new, fork, free, table, n_pages = _batch(rng, 600, 64, 2000, 0, 3000)
+    s = Step(seq, new, free, table, int(new.sum()) + 3, 64, n_pages)
+    if alias != "head":
+        s.out["kv_len"] = s.seq
+    if alias != "lengths":
+        s.out["head"] = s.head_in
+    s.ws[dsa.WS_STATUS_BYTES:] = fill
+    s.call()
+    assert s.check() is not None
+    # a refused batch keeps both
+    s2 = Step(seq, new, free, table, int(new.sum()) - 1, 64, n_pages, alias=True)
+    s2.ws = s.ws
+    s2.ws[dsa.WS_STATUS_BYTES:] = fill
+    s2.call()
+    assert s2.check() is None
