@@ -388,8 +388,9 @@ __global__ void __launch_bounds__(kMlaThreads, 1)
     // everything above touches no input: with programmatic dependent launch
     // it overlaps the end of the kernel that produced the indices
     grid_dependency_wait();
-    // cache rows of this split's entries (invalid entries read row 0 and are
-    // masked; P = 0 there)
+    // cache rows of this split's entries.  Invalid entries read row 0 as keys
+    // (S is masked) and zeros as values: P = 0 there, but 0 * NaN is NaN, and
+    // row 0 may be a row that nobody has written.
     const int n = a.q_n[q];
     const int seq = a.q_seq[q];
     if (a.dense) R = max(min(R, min(n, a.topk) - e0), 0);
@@ -487,7 +488,8 @@ __global__ void __launch_bounds__(kMlaThreads, 1)
                         const uint8_t *vsrc = a.kv8 + static_cast<int64_t>(sm.rows[rr]) * a.kv8_row_bytes;
                         sc = sm.valid[rr] ? a.kv_scale[sm.rows[rr]] : 0.f;
 #pragma unroll
-                        for (int m = 0; m < 8; ++m) b[m] = ldg_u4(vsrc + (vu + 4 * m) * 16);
+                        for (int m = 0; m < 8; ++m)
+                            b[m] = sm.valid[rr] ? ldg_u4(vsrc + (vu + 4 * m) * 16) : make_uint4(0u, 0u, 0u, 0u);
                     };
                     if (nvt > 0) vload(0, cur, csc);
                     for (int vt = 0; vt < nvt; ++vt) {
@@ -523,11 +525,12 @@ __global__ void __launch_bounds__(kMlaThreads, 1)
                             if (ok) {
                                 uint8_t *vdst = vring + v * kVTileBytes + vr * 128;
                                 const uint16_t *vsrc = a.kv + static_cast<int64_t>(sm.rows[vt * kMlaVRows + vr]) * a.kv_row_stride;
+                                const bool vok = sm.valid[vt * kMlaVRows + vr];
 #pragma unroll
                                 for (int m = 0; m < 16; ++m) {
                                     const int pc = vu + 4 * m;  // 16-byte piece of the 512 value columns
                                     const int blk = pc >> 3, j = pc & 7;
-                                    cp_async16(vdst + blk * kVBlockBytes + ((j ^ (vr & 7)) << 4), vsrc + pc * 8);
+                                    cp_async16_or_zero(vdst + blk * kVBlockBytes + ((j ^ (vr & 7)) << 4), vsrc + pc * 8, vok);
                                 }
                             }
                             cp_async_commit();
