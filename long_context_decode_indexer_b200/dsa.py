@@ -8,6 +8,7 @@ call fails, a ``DsaError`` is raised.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 import threading
 from typing import Optional
@@ -310,71 +311,92 @@ def table_workspace_size(tp: TableParams) -> int:
     return int(out.value)
 
 
-def _launch(fn, what, t, stream, *args):
-    """Call `fn` with the device of tensor `t` current, on the caller's stream
-    or that device's current one."""
-    import torch
-    if not t.is_cuda:
-        raise DsaError(DSA_ERR_INVALID_ARG, "%s: tensors must be on a CUDA device" % what)
+def _device(what, t) -> int:
+    """The GPU that tensor `t` of call `what` is on."""
     dev = t.get_device()
+    if dev < 0:
+        raise DsaError(DSA_ERR_INVALID_ARG, "%s: tensors must be on a CUDA device" % what)
+    return dev
+
+
+def _launch(fn, what, dev, stream, *args):
+    """Call `fn` with GPU `dev` current, on the caller's stream or that
+    device's current one."""
     if stream is None:  # the raw handle: a Stream object costs a microsecond a call
-        st = torch._C._cuda_getCurrentRawStream(dev)
+        st = _torch()._C._cuda_getCurrentRawStream(dev)
     else:
         st = stream if isinstance(stream, int) else stream.cuda_stream
-    if dev == torch.cuda.current_device():
+    if dev == _torch()._C._cuda_getDevice():
         _check(fn(*args, st), what)
     else:
-        with torch.cuda.device(dev):
+        with _torch().cuda.device(dev):
             _check(fn(*args, st), what)
 
 
-def _bytes(ws) -> int:
-    if not ws.is_cuda:
-        raise DsaError(DSA_ERR_WORKSPACE, "ws must be on a GPU")
+@functools.lru_cache(maxsize=None)
+def _torch():
+    import torch
+    return torch
+
+
+@functools.lru_cache(maxsize=None)
+def _types(kind):
+    """Element types the bindings take for `kind`; integers of the same size
+    stand for the bits of a 16- or 8-bit float."""
+    t = _torch()
+    return {"i32": frozenset((t.int32, t.uint32)), "fp32": frozenset((t.float32,)),
+            "bf16": frozenset((t.bfloat16, t.int16, t.uint16)), "fp16": frozenset((t.float16, t.int16, t.uint16)),
+            "e4m3": frozenset((t.float8_e4m3fn, t.uint8, t.int8))}[kind]
+
+
+def _refuse(what, need, t, dev):
+    raise DsaError(DSA_ERR_INVALID_ARG, "%s: need %s on GPU %d; got %s %s of strides %s on %s"
+                   % (what, need, dev, t.dtype, tuple(t.shape), tuple(t.stride()), t.device))
+
+
+def _bytes(ws, dev) -> int:
+    if ws.get_device() != dev:
+        raise DsaError(DSA_ERR_WORKSPACE, "ws must be on GPU %d" % dev)
     return ws.numel() * ws.element_size()
 
 
-def _dense(what, t, size, *shape):
-    """The address of a contiguous GPU tensor of `size`-byte elements and this
-    shape (or an address as it is); anything else the call would misread is
-    refused."""
+def _dense(what, t, dev, kind, *shape):
+    """The address of a contiguous tensor of this shape (or an address as it
+    is); anything else the call would misread is refused."""
     if t is None or isinstance(t, int):
         return t
-    if not t.is_cuda or t.element_size() != size or t.shape != shape or not t.is_contiguous():
-        raise DsaError(DSA_ERR_INVALID_ARG, "%s: need %d-byte elements of shape %s, contiguous, on a GPU; got %s %s on %s"
-                       % (what, size, shape, t.dtype, tuple(t.shape), t.device))
+    if t.get_device() != dev or t.dtype not in _types(kind) or t.shape != shape or not t.is_contiguous():
+        _refuse(what, "contiguous %s of shape %s" % (kind, shape), t, dev)
     return t.data_ptr()
 
 
-def _ints(what, t, n):
-    """The address of n adjacent 4-byte elements on a GPU (or an address)."""
+def _list(what, t, dev, n, kind="i32"):
+    """The address of n adjacent 4-byte elements (or an address)."""
     if t is None or isinstance(t, int):
         return t
-    if t.is_cuda and t.numel() == n and t.element_size() == 4 and t.is_contiguous():
+    if t.get_device() == dev and t.dtype in _types(kind) and t.numel() == n and t.is_contiguous():
         return t.data_ptr()
-    raise DsaError(DSA_ERR_INVALID_ARG, "%s: need %d adjacent 4-byte elements on a GPU; got %s %s on %s"
-                   % (what, n, t.dtype, tuple(t.shape), t.device))
+    _refuse(what, "%d adjacent %s" % (n, kind), t, dev)
 
 
-def _sized(what, t, size):
-    """The address of a GPU tensor of `size`-byte elements."""
-    if not t.is_cuda or t.element_size() != size:
-        raise DsaError(DSA_ERR_INVALID_ARG, "%s: need %d-byte elements on a GPU, got %s on %s"
-                       % (what, size, t.dtype, t.device))
+def _sized(what, t, dev, size):
+    """The address of a tensor of `size`-byte elements."""
+    if t.get_device() != dev or t.element_size() != size:
+        _refuse(what, "%d-byte elements" % size, t, dev)
     return t.data_ptr()
 
 
 def build_tables(tp, seq_len, new_len, fork_src, free_pages, free_head, page_table, q_start, q_seq,
                  positions, q_n, slots, kv_len, free_head_out, ws, stream=None):
     """Page tables and slot maps of one step from the requests' lengths."""
-    n, nt = tp.nseq, tp.nt
-    _launch(lib().dsa_build_tables, "dsa_build_tables", q_start, stream, ctypes.byref(tp),
-            _ints("seq_len", seq_len, n), _ints("new_len", new_len, n), _ints("fork_src", fork_src, n),
-            _ints("free_pages", free_pages, tp.n_free), _ints("free_head", free_head, 1),
-            _dense("page_table", page_table, 4, n, tp.max_pages), _ints("q_start", q_start, n + 1),
-            _ints("q_seq", q_seq, nt), _ints("positions", positions, nt), _ints("q_n", q_n, nt),
-            _ints("slots", slots, nt), _ints("kv_len", kv_len, n),
-            _ints("free_head_out", free_head_out, 1), ws.data_ptr(), _bytes(ws))
+    n, nt, dev = tp.nseq, tp.nt, _device("dsa_build_tables", q_start)
+    _launch(lib().dsa_build_tables, "dsa_build_tables", dev, stream, ctypes.byref(tp),
+            _list("seq_len", seq_len, dev, n), _list("new_len", new_len, dev, n), _list("fork_src", fork_src, dev, n),
+            _list("free_pages", free_pages, dev, tp.n_free), _list("free_head", free_head, dev, 1),
+            _dense("page_table", page_table, dev, "i32", n, tp.max_pages), _list("q_start", q_start, dev, n + 1),
+            _list("q_seq", q_seq, dev, nt), _list("positions", positions, dev, nt), _list("q_n", q_n, dev, nt),
+            _list("slots", slots, dev, nt), _list("kv_len", kv_len, dev, n),
+            _list("free_head_out", free_head_out, dev, 1), ws.data_ptr(), _bytes(ws, dev))
 
 
 def make_rope_spec(*, rope_dim=64, layout=ROPE_INTERLEAVED, theta=10000.0, scaling=ROPE_SCALE_NONE, factor=1.0,
@@ -394,9 +416,9 @@ def make_rope_params(*, nt, h, d, dtype, x_heads=None, begin=0, x_strides=None, 
 
 
 def _rope(fn, what, rs, rp, src, positions, dst, stream):
-    size = 4 if rp.dtype == DTYPE_FP32 else 2
-    _launch(fn, what, positions, stream, ctypes.byref(rs), ctypes.byref(rp), _sized("input", src, size),
-            _ints("positions", positions, rp.nt), _sized("output", dst, size))
+    size, dev = 4 if rp.dtype == DTYPE_FP32 else 2, _device(what, positions)
+    _launch(fn, what, dev, stream, ctypes.byref(rs), ctypes.byref(rp), _sized("input", src, dev, size),
+            _list("positions", positions, dev, rp.nt), _sized("output", dst, dev, size))
 
 
 def rope(rs, rp, x, positions, y, stream=None):
@@ -409,31 +431,30 @@ def rope_backward(rs, rp, dy, positions, dx, stream=None):
     _rope(lib().dsa_rope_backward, "dsa_rope_backward", rs, rp, dy, positions, dx, stream)
 
 
-def _part(what, t, nt, width):
+def _part(what, t, dev, nt, width):
     """The address of [nt, width] rows of adjacent 2-byte elements."""
-    if not t.is_cuda or t.element_size() != 2 or t.shape != (nt, width) or (nt > 0 and t.stride(1) != 1):
-        raise DsaError(DSA_ERR_INVALID_ARG, "%s: need 2-byte elements of shape (%d, %d), each row's adjacent, on a "
-                       "GPU; got %s %s on %s" % (what, nt, width, t.dtype, tuple(t.shape), t.device))
+    if t.get_device() != dev or t.element_size() != 2 or t.shape != (nt, width) or (nt > 0 and t.stride(1) != 1):
+        _refuse(what, "2-byte elements of shape (%d, %d), each row's adjacent," % (nt, width), t, dev)
     return t.data_ptr()
 
 
 def latent_append(rs, c_kv, k_pe, positions, slots, kv_cache, ws, stream=None):
     """Append [c_kv | rope(k_pe)] rows to the bf16 latent cache [rows, >= 576]."""
-    nt = slots.shape[0]
-    _launch(lib().dsa_latent_append, "dsa_latent_append", slots, stream, ctypes.byref(rs), nt,
-            _part("c_kv", c_kv, nt, 512), c_kv.stride(0), _part("k_pe", k_pe, nt, 64), k_pe.stride(0),
-            _ints("positions", positions, nt), _ints("slots", slots, nt), _sized("kv_cache", kv_cache, 2),
-            kv_cache.stride(0), kv_cache.shape[0], ws.data_ptr(), _bytes(ws))
+    nt, dev = slots.shape[0], _device("dsa_latent_append", slots)
+    _launch(lib().dsa_latent_append, "dsa_latent_append", dev, stream, ctypes.byref(rs), nt,
+            _part("c_kv", c_kv, dev, nt, 512), c_kv.stride(0), _part("k_pe", k_pe, dev, nt, 64), k_pe.stride(0),
+            _list("positions", positions, dev, nt), _list("slots", slots, dev, nt), _sized("kv_cache", kv_cache, dev, 2),
+            kv_cache.stride(0), kv_cache.shape[0], ws.data_ptr(), _bytes(ws, dev))
 
 
 def latent_append_fp8(rs, c_kv, k_pe, positions, slots, kv8_cache, kv_scale, ws, stream=None):
     """The same into the FP8 latent cache (e4m3 codes, power-of-two row scales)."""
-    nt = slots.shape[0]
-    _launch(lib().dsa_latent_append_fp8, "dsa_latent_append_fp8", slots, stream, ctypes.byref(rs), nt,
-            _part("c_kv", c_kv, nt, 512), c_kv.stride(0), _part("k_pe", k_pe, nt, 64), k_pe.stride(0),
-            _ints("positions", positions, nt), _ints("slots", slots, nt), _sized("kv8_cache", kv8_cache, 1),
-            kv8_cache.stride(0), _ints("kv_scale", kv_scale, kv8_cache.shape[0]), kv8_cache.shape[0],
-            ws.data_ptr(), _bytes(ws))
+    nt, dev = slots.shape[0], _device("dsa_latent_append_fp8", slots)
+    _launch(lib().dsa_latent_append_fp8, "dsa_latent_append_fp8", dev, stream, ctypes.byref(rs), nt,
+            _part("c_kv", c_kv, dev, nt, 512), c_kv.stride(0), _part("k_pe", k_pe, dev, nt, 64), k_pe.stride(0),
+            _list("positions", positions, dev, nt), _list("slots", slots, dev, nt), _sized("kv8_cache", kv8_cache, dev, 1),
+            kv8_cache.stride(0), _list("kv_scale", kv_scale, dev, kv8_cache.shape[0], "fp32"), kv8_cache.shape[0],
+            ws.data_ptr(), _bytes(ws, dev))
 
 
 def shared_prefix_workspace_size(p: Params, kv: KV, ngroups: int) -> int:
@@ -446,11 +467,12 @@ def shared_prefix_workspace_size(p: Params, kv: KV, ngroups: int) -> int:
 def mla_shared_prefix(p, kv, ngroups, group_q0, group_n, q, kv_cache, kv_row_stride, out, lse, ws, stream=None):
     """Dense MLA attention of queries in groups that share a prefix, each
     prefix read once for the whole group."""
-    nq, h = p.nq, p.h
-    _launch(lib().dsa_mla_shared_prefix, "dsa_mla_shared_prefix", group_q0, stream, ctypes.byref(p), ctypes.byref(kv),
-            ngroups, _ints("group_q0", group_q0, ngroups + 1), _ints("group_n", group_n, ngroups),
-            _dense("q", q, 2, nq, h, 576), _ptr(kv_cache), kv_row_stride, _dense("out", out, 2, nq, h, 512),
-            _dense("lse", lse, 4, nq, h), ws.data_ptr(), _bytes(ws))
+    nq, h, dev = p.nq, p.h, _device("dsa_mla_shared_prefix", group_q0)
+    _launch(lib().dsa_mla_shared_prefix, "dsa_mla_shared_prefix", dev, stream, ctypes.byref(p), ctypes.byref(kv),
+            ngroups, _list("group_q0", group_q0, dev, ngroups + 1), _list("group_n", group_n, dev, ngroups),
+            _dense("q", q, dev, "bf16", nq, h, 576), _ptr(kv_cache), kv_row_stride,
+            _dense("out", out, dev, "bf16", nq, h, 512), _dense("lse", lse, dev, "fp32", nq, h), ws.data_ptr(),
+            _bytes(ws, dev))
 
 
 def check_status(ws, stream=None) -> int:

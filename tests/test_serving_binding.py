@@ -1,0 +1,154 @@
+"""What the Python binding of the serving operators hands to the C ABI and
+what it refuses, argument by argument.  The tensors live on the CPU and say
+that they are on GPU 0; the library is a recorder, so nothing is launched."""
+import ctypes
+
+import pytest
+import torch
+
+from long_context_decode_indexer_b200 import dsa
+
+I32, BF16, FP16, FP32, E4M3 = torch.int32, torch.bfloat16, torch.float16, torch.float32, torch.float8_e4m3fn
+
+
+class On:
+    """A CPU tensor that says it is on GPU `dev`."""
+
+    def __init__(self, t, dev=0):
+        self.t, self.dev, self.is_cuda = t, dev, True
+
+    def get_device(self):
+        return self.dev
+
+    def __getattr__(self, name):
+        return getattr(self.t, name)
+
+
+def on(*shape, dtype=I32, dev=0):
+    return On(torch.zeros(shape, dtype=dtype), dev)
+
+
+class Recorder:
+    def __init__(self):
+        self.calls = []
+
+    def __getattr__(self, name):
+        def call(*args):
+            self.calls.append((name, args))
+            return 0
+        return call
+
+
+@pytest.fixture
+def calls(monkeypatch):
+    r = Recorder()
+    monkeypatch.setattr(dsa, "_lib", r)
+    monkeypatch.setattr(torch._C, "_cuda_getDevice", lambda: 0, raising=False)
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
+    return r.calls
+
+
+def refused(name, fn, *args, **kw):
+    """The binding raises for argument `name` and hands nothing on."""
+    with pytest.raises(dsa.DsaError, match=name):
+        fn(*args, stream=0, **kw)
+
+
+# ------------------------------------------------------------------ tables
+TABLE_ARGS = ("seq_len", "new_len", "fork_src", "free_pages", "free_head", "page_table", "q_start", "q_seq",
+              "positions", "q_n", "slots", "kv_len", "free_head_out")
+
+
+def table_args():
+    tp = dsa.make_table_params(nseq=2, nt=3, page_size=64, max_pages=4, n_free=5, cache_rows=6400)
+    size = dict(seq_len=2, new_len=2, fork_src=2, free_pages=5, free_head=1, q_start=3, q_seq=3, positions=3, q_n=3,
+                slots=3, kv_len=2, free_head_out=1)
+    a = {k: on(*((2, 4) if k == "page_table" else (size[k],))) for k in TABLE_ARGS}
+    a["ws"] = on(512, dtype=torch.uint8)
+    return tp, a
+
+
+def test_tables_are_handed_on(calls):
+    tp, a = table_args()
+    dsa.build_tables(tp, **a, stream=0)
+    name, args = calls.pop()
+    assert name == "dsa_build_tables"
+    assert list(args[1:]) == [a[k].data_ptr() for k in TABLE_ARGS] + [a["ws"].data_ptr(), 512, 0]
+    dsa.build_tables(tp, **{**a, "fork_src": None}, stream=0)
+    assert calls.pop()[1][3] is None
+
+
+@pytest.mark.parametrize("name", TABLE_ARGS)
+def test_table_arguments(calls, name):
+    tp, a = table_args()
+    shape = tuple(a[name].shape)
+    more = shape[:-1] + (shape[-1] + 1,)
+    bad = [on(*more), on(*shape, dtype=torch.int64), on(*shape, dtype=FP32), on(*shape, dtype=torch.int16)]
+    if shape[-1] > 1:
+        bad.append(On(torch.zeros(shape[:-1] + (2 * shape[-1],), dtype=I32)[..., ::2]))
+    if name == "page_table":
+        bad += [on(4, 2), On(torch.zeros((4, 2), dtype=I32).t())]
+    if name != "q_start":          # q_start says which GPU the call is for
+        bad += [on(*shape, dev=1), on(*shape, dev=-1)]
+    for t in bad:
+        refused(name, dsa.build_tables, tp, **{**a, name: t})
+    assert not calls
+
+
+def test_cpu_tensors_and_workspaces_elsewhere(calls):
+    tp, a = table_args()
+    refused("CUDA device", dsa.build_tables, tp, **{**a, "q_start": on(3, dev=-1)})
+    for dev in (-1, 1):
+        refused("ws", dsa.build_tables, tp, **{**a, "ws": on(512, dtype=torch.uint8, dev=dev)})
+    assert not calls
+
+
+# -------------------------------------------------------------- other lists
+def test_lists_of_the_other_calls(calls):
+    rs = dsa.make_rope_spec()
+    rp = dsa.make_rope_params(nt=3, h=2, d=64, dtype=dsa.DTYPE_BF16)
+    x, y = on(3, 2, 64, dtype=BF16), on(3, 2, 64, dtype=BF16)
+    c, pe, cache, ws = on(3, 512, dtype=BF16), on(3, 64, dtype=BF16), on(9, 576, dtype=BF16), on(256, dtype=torch.uint8)
+    c8, sc = on(9, 576, dtype=torch.uint8), on(9, dtype=FP32)
+    dsa.rope(rs, rp, x, on(3), y, stream=0)
+    dsa.latent_append(rs, c, pe, on(3), on(3), cache, ws, stream=0)
+    dsa.latent_append_fp8(rs, c, pe, on(3), on(3), c8, sc, ws, stream=0)
+    assert [n for n, _ in calls] == ["dsa_rope", "dsa_latent_append", "dsa_latent_append_fp8"]
+    calls.clear()
+    for bad in (on(4), on(3, dtype=FP32), on(3, dtype=torch.int64)):
+        refused("positions", dsa.rope, rs, rp, x, bad, y)
+        refused("positions", dsa.rope_backward, rs, rp, x, bad, y)
+        refused("positions", dsa.latent_append, rs, c, pe, bad, on(3), cache, ws)
+    refused("slots", dsa.latent_append, rs, c, pe, on(3), on(3, dtype=FP32), cache, ws)
+    refused("kv_scale", dsa.latent_append_fp8, rs, c, pe, on(3), on(3), c8, on(9), ws)
+    refused("kv_scale", dsa.latent_append_fp8, rs, c, pe, on(3), on(3), c8, on(8, dtype=FP32), ws)
+    refused("k_pe", dsa.latent_append, rs, c, on(3, 64, dtype=BF16, dev=1), on(3), on(3), cache, ws)
+    assert not calls
+
+
+def prefix_args():
+    p = dsa.make_params(nq=8, h_idx=64, d_idx=128, h=16, topk=1, max_n=4096, scale=0.04)
+    keep = [torch.zeros(8, dtype=I32), torch.zeros(8, dtype=torch.int64)]
+    kv = dsa.make_kv(q_seq=keep[0], q_n=keep[0], seq_row0=keep[1], cache_rows=30)
+    a = dict(group_q0=on(3), group_n=on(2), q=on(8, 16, 576, dtype=BF16), kv_cache=on(30, 576, dtype=BF16),
+             kv_row_stride=576, out=on(8, 16, 512, dtype=BF16), lse=on(8, 16, dtype=FP32), ws=on(1024, dtype=torch.uint8))
+    return p, kv, a, keep
+
+
+def test_shared_prefix_arguments(calls):
+    p, kv, a, keep = prefix_args()
+    dsa.mla_shared_prefix(p, kv, 2, **a, stream=0)
+    args = calls.pop()[1]
+    assert [x for x in args[2:]] == [2] + [a[k].data_ptr() if k != "kv_row_stride" else 576 for k in
+                                           ("group_q0", "group_n", "q", "kv_cache", "kv_row_stride", "out", "lse", "ws")] + [1024, 0]
+    bad = dict(group_q0=[on(2), on(3, dtype=FP32)], group_n=[on(3), on(2, dtype=FP32), on(2, dev=1)],
+               q=[on(8, 16, 576, dtype=FP16), on(16, 8, 576, dtype=BF16), on(8, 16, 512, dtype=BF16),
+                  On(torch.zeros((16, 8, 576), dtype=BF16).transpose(0, 1)), on(8, 16, 576, dtype=BF16, dev=-1)],
+               out=[on(8, 16, 512, dtype=FP16), on(8, 16, 576, dtype=BF16), on(8, 16, 512, dtype=FP32)],
+               lse=[on(8, 16, dtype=BF16), on(16, 8, dtype=FP32), on(8, 16)])
+    for name, ts in bad.items():
+        for t in ts:
+            refused(name, dsa.mla_shared_prefix, p, kv, 2, **{**a, name: t})
+    # raw bits of bf16 pass, as everywhere in the binding
+    dsa.mla_shared_prefix(p, kv, 2, **{**a, "q": on(8, 16, 576, dtype=torch.int16)}, stream=0)
+    assert len(calls) == 1
