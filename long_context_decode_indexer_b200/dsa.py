@@ -386,6 +386,32 @@ def _sized(what, t, dev, size):
     return t.data_ptr()
 
 
+def _heads(what, t, dev, kind, nt, heads, d, ts, hs):
+    """The address of the rows [nt, heads, d] whose tokens are `ts` and heads
+    `hs` elements apart.  `t` is that view itself (or more tokens of it), the
+    same with heads and elements joined, [.., heads * d], or a flat buffer."""
+    if t.get_device() == dev and t.dtype in _types(kind):
+        shape, strides = t.shape, t.stride()
+        if nt == 0:
+            return t.data_ptr()
+        if len(shape) == 3 and shape[1] == heads and shape[2] == d:
+            if shape[0] >= nt and (nt == 1 or strides[0] == ts) and (heads == 1 or strides[1] == hs) and \
+                    (d == 1 or strides[2] == 1):
+                return t.data_ptr()
+        elif len(shape) == 2 and shape[1] == heads * d:
+            if shape[0] >= nt and (nt == 1 or strides[0] == ts) and (heads == 1 or hs == d) and \
+                    (shape[1] == 1 or strides[1] == 1):
+                return t.data_ptr()
+        elif t.is_contiguous():
+            if len(shape) == 1:
+                if t.numel() >= (nt - 1) * ts + (heads - 1) * hs + d:
+                    return t.data_ptr()
+            elif t.numel() == nt * heads * d and (nt == 1 or ts == heads * d) and (heads == 1 or hs == d) and \
+                    (shape[-1] == heads * d or shape[-2:] == (heads, d)):
+                return t.data_ptr()
+    _refuse(what, "%s rows [%d, %d, %d] of strides (%d, %d, 1)" % (kind, nt, heads, d, ts, hs), t, dev)
+
+
 def build_tables(tp, seq_len, new_len, fork_src, free_pages, free_head, page_table, q_start, q_seq,
                  positions, q_n, slots, kv_len, free_head_out, ws, stream=None):
     """Page tables and slot maps of one step from the requests' lengths."""
@@ -415,20 +441,29 @@ def make_rope_params(*, nt, h, d, dtype, x_heads=None, begin=0, x_strides=None, 
                       int(x_strides[1]), int(y_strides[0]), int(y_strides[1]))
 
 
-def _rope(fn, what, rs, rp, src, positions, dst, stream):
-    size, dev = 4 if rp.dtype == DTYPE_FP32 else 2, _device(what, positions)
-    _launch(fn, what, dev, stream, ctypes.byref(rs), ctypes.byref(rp), _sized("input", src, dev, size),
-            _list("positions", positions, dev, rp.nt), _sized("output", dst, dev, size))
+_ROPE_KINDS = ("bf16", "fp16", "fp32")
+
+
+def _rope(fn, what, rs, rp, src, positions, dst, stream, backward):
+    if not 0 <= rp.dtype <= 2:
+        raise DsaError(DSA_ERR_INVALID_ARG, "%s: unknown dtype %d" % (what, rp.dtype))
+    dev, kind, nt, d = _device(what, positions), _ROPE_KINDS[rp.dtype], rp.nt, rp.d
+    x, y = (dst, src) if backward else (src, dst)
+    xp = _heads("dx" if backward else "x", x, dev, kind, nt, rp.x_heads, d, rp.x_token_stride, rp.x_head_stride)
+    yp = _heads("dy" if backward else "y", y, dev, kind, nt, rp.h, d, rp.y_token_stride, rp.y_head_stride)
+    _launch(fn, what, dev, stream, ctypes.byref(rs), ctypes.byref(rp), yp if backward else xp,
+            _list("positions", positions, dev, nt), xp if backward else yp)
 
 
 def rope(rs, rp, x, positions, y, stream=None):
-    """Rotary positions: y = x with its rotated range turned (y may be x)."""
-    _rope(lib().dsa_rope, "dsa_rope", rs, rp, x, positions, y, stream)
+    """Rotary positions: y = x with its rotated range turned (y may be x).
+    x and y are [nt, x_heads, d] and [nt, h, d] with rp's strides."""
+    _rope(lib().dsa_rope, "dsa_rope", rs, rp, x, positions, y, stream, False)
 
 
 def rope_backward(rs, rp, dy, positions, dx, stream=None):
     """Gradient of rope (summed over the heads of a shared x)."""
-    _rope(lib().dsa_rope_backward, "dsa_rope_backward", rs, rp, dy, positions, dx, stream)
+    _rope(lib().dsa_rope_backward, "dsa_rope_backward", rs, rp, dy, positions, dx, stream, True)
 
 
 def _part(what, t, dev, nt, width):

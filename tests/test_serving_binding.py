@@ -152,3 +152,65 @@ def test_shared_prefix_arguments(calls):
     # raw bits of bf16 pass, as everywhere in the binding
     dsa.mla_shared_prefix(p, kv, 2, **{**a, "q": on(8, 16, 576, dtype=torch.int16)}, stream=0)
     assert len(calls) == 1
+
+
+# -------------------------------------------------------------------- rope
+DT = {dsa.DTYPE_BF16: BF16, dsa.DTYPE_FP16: FP16, dsa.DTYPE_FP32: FP32}
+
+
+def rope_call(rp, x, y, backward):
+    if backward:
+        dsa.rope_backward(dsa.make_rope_spec(), rp, y, on(rp.nt), x, stream=0)
+    else:
+        dsa.rope(dsa.make_rope_spec(), rp, x, on(rp.nt), y, stream=0)
+
+
+@pytest.mark.parametrize("backward", [False, True])
+@pytest.mark.parametrize("dtype", list(DT))
+def test_rotated_tensors_that_are_as_described(calls, dtype, backward):
+    z = lambda *s: torch.zeros(s, dtype=DT[dtype])
+    dense = dsa.make_rope_params(nt=6, h=4, d=64, dtype=dtype)
+    wide = z(6, 4, 192)
+    views = dsa.make_rope_params(nt=6, h=4, d=64, dtype=dtype, x_strides=(768, 192), y_strides=(768, 192))
+    row = z(6, 576)
+    shared = dsa.make_rope_params(nt=6, h=4, x_heads=1, d=64, dtype=dtype, x_strides=(576, 64))
+    joined = z(6, 300)
+    wide_row = dsa.make_rope_params(nt=6, h=4, d=64, dtype=dtype, x_strides=(300, 64))
+    one = dsa.make_rope_params(nt=1, h=1, d=64, dtype=dtype, x_strides=(7, 9), y_strides=(0, 0))
+    for rp, x, y in ((dense, z(6, 4, 64), z(6, 4, 64)), (dense, z(9, 4, 64), z(6, 256)),
+                     (dense, z(2, 3, 4, 64), z(2, 3, 256)), (dense, z(6 * 256), z(7 * 256)),
+                     (views, wide[..., 128:], wide[..., 128:]), (shared, row[:, 512:], z(6, 4, 64)),
+                     (shared, row[:, None, 512:], z(6, 4, 64)), (wide_row, joined[:, :256], z(6, 4, 64)),
+                     (one, z(1, 1, 64), z(1, 64))):
+        rope_call(rp, On(x), On(y), backward)
+        args = calls.pop()[1]
+        assert args[2] == (y if backward else x).data_ptr() and args[4] == (x if backward else y).data_ptr()
+    if dtype != dsa.DTYPE_FP32:          # raw bits
+        rope_call(dense, On(z(6, 4, 64).view(torch.int16)), On(z(6, 4, 64)), backward)
+    rope_call(dsa.make_rope_params(nt=0, h=4, d=64, dtype=dtype), On(z(0, 4, 64)), On(z(0, 4, 64)), backward)
+
+
+@pytest.mark.parametrize("backward", [False, True])
+@pytest.mark.parametrize("side", ["x", "y"])
+def test_rotated_tensors_that_would_be_misread(calls, side, backward):
+    z = lambda *s, dtype=BF16: torch.zeros(s, dtype=dtype)
+    rp = dsa.make_rope_params(nt=6, h=4, d=64, dtype=dsa.DTYPE_BF16)
+    name = ("d" if backward else "") + side
+    bad = [On(z(6, 4, 192)[..., 128:]),            # a slice, described as dense
+           On(z(4, 6, 64)), On(z(4, 6, 64).transpose(0, 1)), On(z(6, 64, 4).transpose(1, 2)),
+           On(z(5, 4, 64)), On(z(6, 4, 63)), On(z(6, 3, 64)), On(z(6, 128)), On(z(6 * 256 - 1)),
+           On(z(6, 4, 128)[..., ::2]), On(z(1, 4, 64).expand(6, 4, 64)), On(z(6, 8, 64)[:, ::2]),
+           On(z(2, 3, 4, 128)[..., :64]), On(z(3, 4, 64)), On(z(24, 64)),
+           On(z(6, 4, 64, dtype=FP16)), On(z(6, 4, 64, dtype=FP32)), On(z(6, 4, 64, dtype=torch.int32)),
+           On(z(6, 4, 64), dev=1), On(z(6, 4, 64), dev=-1)]
+    ok = On(z(6, 4, 64))
+    for t in bad:
+        with pytest.raises(dsa.DsaError, match="^" + name + ":"):
+            rope_call(rp, t if side == "x" else ok, t if side == "y" else ok, backward)
+    # a short buffer for strides that reach past it
+    far = dsa.make_rope_params(nt=6, h=4, d=64, dtype=dsa.DTYPE_BF16, x_strides=(512, 64), y_strides=(512, 64))
+    with pytest.raises(dsa.DsaError, match="^" + name + ":"):
+        rope_call(far, On(z(6 * 256) if side == "x" else z(6 * 512)), On(z(6 * 256) if side == "y" else z(6 * 512)), backward)
+    assert not calls
+    with pytest.raises(dsa.DsaError, match="dtype"):
+        rope_call(dsa.make_rope_params(nt=6, h=4, d=64, dtype=3), ok, ok, backward)
