@@ -379,13 +379,6 @@ def _list(what, t, dev, n, kind="i32"):
     _refuse(what, "%d adjacent %s" % (n, kind), t, dev)
 
 
-def _sized(what, t, dev, size):
-    """The address of a tensor of `size`-byte elements."""
-    if t.get_device() != dev or t.element_size() != size:
-        _refuse(what, "%d-byte elements" % size, t, dev)
-    return t.data_ptr()
-
-
 def _heads(what, t, dev, kind, nt, heads, d, ts, hs):
     """The address of the rows [nt, heads, d] whose tokens are `ts` and heads
     `hs` elements apart.  `t` is that view itself (or more tokens of it), the
@@ -467,29 +460,40 @@ def rope_backward(rs, rp, dy, positions, dx, stream=None):
 
 
 def _part(what, t, dev, nt, width):
-    """The address of [nt, width] rows of adjacent 2-byte elements."""
-    if t.get_device() != dev or t.element_size() != 2 or t.shape != (nt, width) or (nt > 0 and t.stride(1) != 1):
-        _refuse(what, "2-byte elements of shape (%d, %d), each row's adjacent," % (nt, width), t, dev)
+    """The address of [nt, width] bf16 rows, each one's elements adjacent."""
+    if t.get_device() != dev or t.dtype not in _types("bf16") or t.shape != (nt, width) or (nt > 0 and t.stride(1) != 1):
+        _refuse(what, "bf16 rows [%d, %d], each one's elements adjacent," % (nt, width), t, dev)
     return t.data_ptr()
+
+
+def _cache(what, t, dev, kind):
+    """The address and row stride of a latent cache [rows, >= 576]."""
+    if t.get_device() == dev and t.dtype in _types(kind) and t.dim() == 2 and t.shape[1] >= 576:
+        stride, inner = t.stride()
+        if inner == 1:
+            return t.data_ptr(), stride
+    _refuse(what, "%s rows [rows, >= 576], each one's elements adjacent," % kind, t, dev)
 
 
 def latent_append(rs, c_kv, k_pe, positions, slots, kv_cache, ws, stream=None):
     """Append [c_kv | rope(k_pe)] rows to the bf16 latent cache [rows, >= 576]."""
     nt, dev = slots.shape[0], _device("dsa_latent_append", slots)
+    cache, stride = _cache("kv_cache", kv_cache, dev, "bf16")
     _launch(lib().dsa_latent_append, "dsa_latent_append", dev, stream, ctypes.byref(rs), nt,
             _part("c_kv", c_kv, dev, nt, 512), c_kv.stride(0), _part("k_pe", k_pe, dev, nt, 64), k_pe.stride(0),
-            _list("positions", positions, dev, nt), _list("slots", slots, dev, nt), _sized("kv_cache", kv_cache, dev, 2),
-            kv_cache.stride(0), kv_cache.shape[0], ws.data_ptr(), _bytes(ws, dev))
+            _list("positions", positions, dev, nt), _list("slots", slots, dev, nt), cache, stride, kv_cache.shape[0],
+            ws.data_ptr(), _bytes(ws, dev))
 
 
 def latent_append_fp8(rs, c_kv, k_pe, positions, slots, kv8_cache, kv_scale, ws, stream=None):
-    """The same into the FP8 latent cache (e4m3 codes, power-of-two row scales)."""
+    """The same into the FP8 latent cache [rows, >= 576] (e4m3 codes, power-of-two row scales)."""
     nt, dev = slots.shape[0], _device("dsa_latent_append_fp8", slots)
+    rows = kv8_cache.shape[0]
+    cache, stride = _cache("kv8_cache", kv8_cache, dev, "e4m3")
     _launch(lib().dsa_latent_append_fp8, "dsa_latent_append_fp8", dev, stream, ctypes.byref(rs), nt,
             _part("c_kv", c_kv, dev, nt, 512), c_kv.stride(0), _part("k_pe", k_pe, dev, nt, 64), k_pe.stride(0),
-            _list("positions", positions, dev, nt), _list("slots", slots, dev, nt), _sized("kv8_cache", kv8_cache, dev, 1),
-            kv8_cache.stride(0), _list("kv_scale", kv_scale, dev, kv8_cache.shape[0], "fp32"), kv8_cache.shape[0],
-            ws.data_ptr(), _bytes(ws, dev))
+            _list("positions", positions, dev, nt), _list("slots", slots, dev, nt), cache, stride,
+            _list("kv_scale", kv_scale, dev, rows, "fp32"), rows, ws.data_ptr(), _bytes(ws, dev))
 
 
 def shared_prefix_workspace_size(p: Params, kv: KV, ngroups: int) -> int:

@@ -214,3 +214,39 @@ def test_rotated_tensors_that_would_be_misread(calls, side, backward):
     assert not calls
     with pytest.raises(dsa.DsaError, match="dtype"):
         rope_call(dsa.make_rope_params(nt=6, h=4, d=64, dtype=3), ok, ok, backward)
+
+
+# ------------------------------------------------------------------ append
+@pytest.mark.parametrize("fp8", [False, True])
+def test_append_caches(calls, fp8):
+    dt = torch.uint8 if fp8 else BF16
+    ws, sc = on(256, dtype=torch.uint8), on(64, dtype=FP32)
+    kv_a = torch.zeros((3, 576), dtype=BF16)
+    name = "kv8_cache" if fp8 else "kv_cache"
+
+    def append(cache, c=On(kv_a[:, :512]), pe=On(kv_a[:, 512:])):
+        if fp8:
+            dsa.latent_append_fp8(dsa.make_rope_spec(), c, pe, on(3), on(3), cache, sc, ws, stream=0)
+        else:
+            dsa.latent_append(dsa.make_rope_spec(), c, pe, on(3), on(3), cache, ws, stream=0)
+
+    z = lambda *s, dtype=dt: torch.zeros(s, dtype=dtype)
+    good = [z(64, 576), z(64, 640), z(64, 640)[:, :576], z(64, 704)[:, 64:]]
+    good += [z(64, 576, dtype=E4M3)] if fp8 else [z(64, 576, dtype=torch.int16)]
+    for t in good:
+        append(On(t))
+        args = calls.pop()[1]
+        assert args[8:10] == (t.data_ptr(), t.stride(0)) and args[-4] == 64
+        assert args[2:6] == (kv_a.data_ptr(), 576, kv_a.data_ptr() + 1024, 576)
+    bad = [z(4, 16, 576),                       # pages: rows of one would be 16 apart
+           z(64, 512), z(640, 64).t(), z(64, 1152)[:, ::2], z(64 * 576), z(64, 640)[:, 128:],
+           z(64, 576, dtype=FP16), z(64, 576, dtype=FP32), z(64, 576, dtype=BF16 if fp8 else torch.uint8)]
+    for t in [On(t) for t in bad] + [on(64, 576, dtype=dt, dev=1), on(64, 576, dtype=dt, dev=-1)]:
+        with pytest.raises(dsa.DsaError, match="^%s:" % name):
+            append(t)
+    for part, w in (("c_kv", 512), ("k_pe", 64)):
+        for t in (z(3, w, dtype=FP16), z(3, w + 8, dtype=BF16), z(4, w, dtype=BF16), z(w, 3, dtype=BF16).t(),
+                  z(3, w, 1, dtype=BF16)):
+            with pytest.raises(dsa.DsaError, match="^%s:" % part):
+                append(On(good[0]), **{"c" if part == "c_kv" else "pe": On(t)})
+    assert not calls
