@@ -475,6 +475,24 @@ def _cache(what, t, dev, kind):
     _refuse(what, "%s rows [rows, >= 576], each one's elements adjacent," % kind, t, dev)
 
 
+def _cache_rows(what, t, dev, kind, rows, row_stride):
+    """The address of a latent cache of `rows` rows, `row_stride` elements
+    apart: rows [rows, >= 576], pages [pages, page_size, >= 576] that lie one
+    behind the other, or a flat buffer (or an address)."""
+    if isinstance(t, int):
+        return t
+    if t.get_device() == dev and t.dtype in _types(kind):
+        shape, strides = t.shape, t.stride()
+        if len(shape) == 1:
+            if strides[0] == 1 and shape[0] >= (rows - 1) * row_stride + 576:
+                return t.data_ptr()
+        elif shape[-1] >= 576 and strides[-1] == 1 and strides[-2] == row_stride:
+            if len(shape) == 2 and shape[0] >= rows or \
+                    len(shape) == 3 and shape[0] * shape[1] >= rows and strides[0] == shape[1] * row_stride:
+                return t.data_ptr()
+    _refuse(what, "%s, %d rows of >= 576 elements, %d apart," % (kind, rows, row_stride), t, dev)
+
+
 def latent_append(rs, c_kv, k_pe, positions, slots, kv_cache, ws, stream=None):
     """Append [c_kv | rope(k_pe)] rows to the bf16 latent cache [rows, >= 576]."""
     nt, dev = slots.shape[0], _device("dsa_latent_append", slots)
@@ -509,7 +527,8 @@ def mla_shared_prefix(p, kv, ngroups, group_q0, group_n, q, kv_cache, kv_row_str
     nq, h, dev = p.nq, p.h, _device("dsa_mla_shared_prefix", group_q0)
     _launch(lib().dsa_mla_shared_prefix, "dsa_mla_shared_prefix", dev, stream, ctypes.byref(p), ctypes.byref(kv),
             ngroups, _list("group_q0", group_q0, dev, ngroups + 1), _list("group_n", group_n, dev, ngroups),
-            _dense("q", q, dev, "bf16", nq, h, 576), _ptr(kv_cache), kv_row_stride,
+            _dense("q", q, dev, "bf16", nq, h, 576),
+            _cache_rows("kv_cache", kv_cache, dev, "bf16", kv.cache_rows, kv_row_stride), kv_row_stride,
             _dense("out", out, dev, "bf16", nq, h, 512), _dense("lse", lse, dev, "fp32", nq, h), ws.data_ptr(),
             _bytes(ws, dev))
 

@@ -250,3 +250,24 @@ def test_append_caches(calls, fp8):
             with pytest.raises(dsa.DsaError, match="^%s:" % part):
                 append(On(good[0]), **{"c" if part == "c_kv" else "pe": On(t)})
     assert not calls
+
+
+# ----------------------------------------------------------- shared prefix
+def test_shared_prefix_caches(calls):
+    p, kv, a, keep = prefix_args()          # 30 rows
+    z = lambda *s, dtype=BF16: torch.zeros(s, dtype=dtype)
+    for t, stride in ((z(30, 576), 576), (z(31, 640), 640), (z(30, 640)[:, :576], 640), (z(2, 15, 576), 576),
+                      (z(29 * 584 + 576), 584), (z(30, 576, dtype=torch.int16), 576)):
+        dsa.mla_shared_prefix(p, kv, 2, **{**a, "kv_cache": On(t), "kv_row_stride": stride}, stream=0)
+        assert calls.pop()[1][6:8] == (t.data_ptr(), stride)
+    bad = [(on(30, 576, dtype=torch.uint8), 576),       # an FP8 cache: rows half as long
+           (on(30, 576, dtype=E4M3), 576), (on(30, 576, dtype=FP16), 576), (on(30, 576, dtype=FP32), 576),
+           (on(30, 576, dtype=BF16, dev=-1), 576), (on(30, 576, dtype=BF16, dev=1), 576),
+           (on(29, 576, dtype=BF16), 576), (on(30, 640, dtype=BF16), 576), (on(30, 576, dtype=BF16), 640),
+           (on(30, 512, dtype=BF16), 512), (on(29 * 576 + 575, dtype=BF16), 576), (on(30, 1, 576, dtype=BF16), 640),
+           (On(z(2, 20, 576)[:, :15]), 576), (On(z(576, 30).t()), 576), (On(z(30, 1152)[:, ::2]), 1152)]
+    for t, stride in bad:
+        refused("kv_cache", dsa.mla_shared_prefix, p, kv, 2, **{**a, "kv_cache": t, "kv_row_stride": stride})
+    assert not calls
+    dsa.mla_shared_prefix(p, kv, 2, **{**a, "kv_cache": 1 << 20}, stream=0)     # an address, as it is
+    assert calls.pop()[1][6] == 1 << 20
