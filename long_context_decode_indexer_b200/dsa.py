@@ -479,7 +479,7 @@ def _cache_rows(what, t, dev, kind, rows, row_stride):
     """The address of a latent cache of `rows` rows, `row_stride` elements
     apart: rows [rows, >= 576], pages [pages, page_size, >= 576] that lie one
     behind the other, or a flat buffer (or an address)."""
-    if isinstance(t, int):
+    if t is None or isinstance(t, int):
         return t
     if t.get_device() == dev and t.dtype in _types(kind):
         shape, strides = t.shape, t.stride()

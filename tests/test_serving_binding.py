@@ -271,3 +271,10 @@ def test_shared_prefix_caches(calls):
     assert not calls
     dsa.mla_shared_prefix(p, kv, 2, **{**a, "kv_cache": 1 << 20}, stream=0)     # an address, as it is
     assert calls.pop()[1][6] == 1 << 20
+
+
+def test_shared_prefix_of_no_queries_needs_no_tensors(calls):
+    p, kv, a, keep = prefix_args()
+    p = dsa.make_params(nq=0, h_idx=64, d_idx=128, h=16, topk=1, max_n=4096, scale=0.04)
+    dsa.mla_shared_prefix(p, kv, 0, on(1), None, None, None, 576, None, None, a["ws"], stream=0)
+    assert calls.pop()[1][5:8] == (None, None, 576)
