@@ -2,9 +2,11 @@
 //
 // Pair i of a head turns by the angle pos * f_i.  The host passes f_i / 2 pi
 // in 64 bits (the scaling for long contexts is all in these numbers), so a
-// thread gets an angle from one 64-bit product: its fractional part, in turns,
-// is exact to 2^-53 * pos * f_i (2e-9 of a turn at position 10^7 and f = 1),
-// and sincospif does the rest in fp32.  No table of cosines is read or kept.
+// thread gets an angle from one 64-bit product.  The speed's own rounding and
+// the product's leave a few 2^-53 of the angle: 2e-8 rad at position 2^27 and
+// f = 1, a third of an fp32 step.  sincospif takes its fractional part rounded
+// to fp32, and what that rounding left out (up to 9e-8 rad) turns the result
+// once more, to first order.  No table of cosines is read or kept.
 //
 // All three kernels move bytes and little else: the floor is x read and y
 // written once.
@@ -68,8 +70,13 @@ __device__ __forceinline__ void store_pack(T *p, const Pack<T, N> &r) {
 
 // sin and cos of pos * turn turns.
 __device__ __forceinline__ void turn_sincos(int pos, double turn, float &s, float &c) {
-    const double t = static_cast<double>(pos) * turn;
-    sincospif(2.f * static_cast<float>(t - rint(t)), &s, &c);
+    const double t = static_cast<double>(pos) * turn, half_turns = 2.0 * (t - rint(t));
+    const float near = static_cast<float>(half_turns);
+    float s0, c0;
+    sincospif(near, &s0, &c0);
+    const float rest = static_cast<float>(half_turns - near) * 3.14159265f;  // radians
+    s = fmaf(c0, rest, s0);
+    c = fmaf(-s0, rest, c0);
 }
 
 }  // namespace
