@@ -453,7 +453,8 @@ int dsa_build_tables(const dsa_table_params *tp, const int32_t *seq_len, const i
  * in fp32 from angles reduced in 64 bits: they are off by about 2^-24 and by
  * at most 8 * 2^-53 of the angle pos * f_i itself (rarely a third of that).
  * For speeds up to 1 that is fp32 accuracy for positions up to 2^27, the
- * longest history any call takes; at 2^31 - 1 it is about 4e-7. */
+ * longest history any call takes; at 2^31 - 1 it is about 4e-7.  A theta and
+ * factor whose speeds exceed 1e290 are refused. */
 enum { DSA_ROPE_INTERLEAVED = 0, DSA_ROPE_HALF = 1 };
 enum { DSA_ROPE_SCALE_NONE = 0, DSA_ROPE_SCALE_LINEAR = 1, DSA_ROPE_SCALE_BASE = 2, DSA_ROPE_SCALE_YARN = 3 };
 enum { DSA_DTYPE_BF16 = 0, DSA_DTYPE_FP16 = 1, DSA_DTYPE_FP32 = 2 };

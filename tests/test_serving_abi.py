@@ -192,3 +192,13 @@ def test_binding_refuses_what_the_call_would_misread(L):
                               FAKE, FAKE, ws)
     with pytest.raises(dsa.DsaError):
         dsa.mla_shared_prefix(par(), kvd(), 2, i32(2), i32(2), FAKE, FAKE, 576, FAKE, FAKE, ws)
+
+
+@pytest.mark.parametrize("kw", [dict(scaling=dsa.ROPE_SCALE_LINEAR, factor=1e-300),
+                                dict(rope_dim=256, theta=1e-300), dict(scaling=dsa.ROPE_SCALE_BASE, factor=1e-300),
+                                dict(scaling=dsa.ROPE_SCALE_YARN, factor=1e-306, orig_max_pos=4096)])
+def test_speeds_that_are_not_finite_are_refused(L, kw):
+    """Their sines would be NaN."""
+    assert rope(L, {"rope_dim": 64, **kw}) == dsa.DSA_ERR_INVALID_ARG
+    if kw.get("rope_dim", 64) == 64:
+        assert append(L, kw) == dsa.DSA_ERR_INVALID_ARG
