@@ -322,15 +322,18 @@ def _device(what, t) -> int:
 def _launch(fn, what, dev, stream, *args):
     """Call `fn` with GPU `dev` current, on the caller's stream or that
     device's current one."""
+    torch = _torch()
     if stream is None:  # the raw handle: a Stream object costs a microsecond a call
-        st = _torch()._C._cuda_getCurrentRawStream(dev)
+        st = torch._C._cuda_getCurrentRawStream(dev)
     else:
         st = stream if isinstance(stream, int) else stream.cuda_stream
-    if dev == _torch()._C._cuda_getDevice():
-        _check(fn(*args, st), what)
+    if dev == torch._C._cuda_getDevice():
+        rc = fn(*args, st)
     else:
-        with _torch().cuda.device(dev):
-            _check(fn(*args, st), what)
+        with torch.cuda.device(dev):
+            rc = fn(*args, st)
+    if rc:
+        _check(rc, what)
 
 
 @functools.lru_cache(maxsize=None)
@@ -341,9 +344,13 @@ def _torch():
 
 @functools.lru_cache(maxsize=None)
 def _types(kind):
-    """Element types the bindings take for `kind`; integers of the same size
-    stand for the bits of a 16- or 8-bit float."""
+    """Element types the bindings take for `kind` (a name, or a dtype of the
+    rotation); integers of the same size stand for the bits of a 16- or 8-bit
+    float."""
     t = _torch()
+    kind = {DTYPE_BF16: "bf16", DTYPE_FP16: "fp16", DTYPE_FP32: "fp32"}.get(kind, kind)
+    if isinstance(kind, int):
+        raise DsaError(DSA_ERR_INVALID_ARG, "unknown dtype %d" % kind)
     return {"i32": frozenset((t.int32, t.uint32)), "fp32": frozenset((t.float32,)),
             "bf16": frozenset((t.bfloat16, t.int16, t.uint16)), "fp16": frozenset((t.float16, t.int16, t.uint16)),
             "e4m3": frozenset((t.float8_e4m3fn, t.uint8, t.int8))}[kind]
@@ -384,7 +391,10 @@ def _heads(what, t, dev, kind, nt, heads, d, ts, hs):
     `hs` elements apart.  `t` is that view itself (or more tokens of it), the
     same with heads and elements joined, [.., heads * d], or a flat buffer."""
     if t.get_device() == dev and t.dtype in _types(kind):
-        shape, strides = t.shape, t.stride()
+        shape = t.shape
+        if shape == (nt, heads, d) and hs == d and ts == heads * d and t.is_contiguous():
+            return t.data_ptr()   # the usual call
+        strides = t.stride()
         if nt == 0:
             return t.data_ptr()
         if len(shape) == 3 and shape[1] == heads and shape[2] == d:
@@ -402,7 +412,7 @@ def _heads(what, t, dev, kind, nt, heads, d, ts, hs):
             elif t.numel() == nt * heads * d and (nt == 1 or ts == heads * d) and (heads == 1 or hs == d) and \
                     (shape[-1] == heads * d or shape[-2:] == (heads, d)):
                 return t.data_ptr()
-    _refuse(what, "%s rows [%d, %d, %d] of strides (%d, %d, 1)" % (kind, nt, heads, d, ts, hs), t, dev)
+    _refuse(what, "%s rows [%d, %d, %d] of strides (%d, %d, 1)" % (("bf16", "fp16", "fp32")[kind], nt, heads, d, ts, hs), t, dev)
 
 
 def build_tables(tp, seq_len, new_len, fork_src, free_pages, free_head, page_table, q_start, q_seq,
@@ -434,16 +444,11 @@ def make_rope_params(*, nt, h, d, dtype, x_heads=None, begin=0, x_strides=None, 
                       int(x_strides[1]), int(y_strides[0]), int(y_strides[1]))
 
 
-_ROPE_KINDS = ("bf16", "fp16", "fp32")
-
-
 def _rope(fn, what, rs, rp, src, positions, dst, stream, backward):
-    if not 0 <= rp.dtype <= 2:
-        raise DsaError(DSA_ERR_INVALID_ARG, "%s: unknown dtype %d" % (what, rp.dtype))
-    dev, kind, nt, d = _device(what, positions), _ROPE_KINDS[rp.dtype], rp.nt, rp.d
+    dev, kind, nt, h, d = _device(what, positions), rp.dtype, rp.nt, rp.h, rp.d
     x, y = (dst, src) if backward else (src, dst)
     xp = _heads("dx" if backward else "x", x, dev, kind, nt, rp.x_heads, d, rp.x_token_stride, rp.x_head_stride)
-    yp = _heads("dy" if backward else "y", y, dev, kind, nt, rp.h, d, rp.y_token_stride, rp.y_head_stride)
+    yp = _heads("dy" if backward else "y", y, dev, kind, nt, h, d, rp.y_token_stride, rp.y_head_stride)
     _launch(fn, what, dev, stream, ctypes.byref(rs), ctypes.byref(rp), yp if backward else xp,
             _list("positions", positions, dev, nt), xp if backward else yp)
 
