@@ -377,13 +377,16 @@ def _dense(what, t, dev, kind, *shape):
     return t.data_ptr()
 
 
-def _list(what, t, dev, n, kind="i32"):
+def _list(what, t, dev, n, kinds):
     """The address of n adjacent 4-byte elements (or an address)."""
-    if t is None or isinstance(t, int):
-        return t
-    if t.get_device() == dev and t.dtype in _types(kind) and t.numel() == n and t.is_contiguous():
-        return t.data_ptr()
-    _refuse(what, "%d adjacent %s" % (n, kind), t, dev)
+    try:
+        if t.get_device() == dev and t.dtype in kinds and t.numel() == n and t.is_contiguous():
+            return t.data_ptr()
+    except AttributeError:
+        if t is None or isinstance(t, int):
+            return t
+        raise
+    _refuse(what, "%d adjacent %s" % (n, "/".join(sorted(str(k) for k in kinds))), t, dev)
 
 
 def _heads(what, t, dev, kind, nt, heads, d, ts, hs):
@@ -418,14 +421,15 @@ def _heads(what, t, dev, kind, nt, heads, d, ts, hs):
 def build_tables(tp, seq_len, new_len, fork_src, free_pages, free_head, page_table, q_start, q_seq,
                  positions, q_n, slots, kv_len, free_head_out, ws, stream=None):
     """Page tables and slot maps of one step from the requests' lengths."""
-    n, nt, dev = tp.nseq, tp.nt, _device("dsa_build_tables", q_start)
+    n, nt, dev, i32 = tp.nseq, tp.nt, _device("dsa_build_tables", q_start), _types("i32")
     _launch(lib().dsa_build_tables, "dsa_build_tables", dev, stream, ctypes.byref(tp),
-            _list("seq_len", seq_len, dev, n), _list("new_len", new_len, dev, n), _list("fork_src", fork_src, dev, n),
-            _list("free_pages", free_pages, dev, tp.n_free), _list("free_head", free_head, dev, 1),
-            _dense("page_table", page_table, dev, "i32", n, tp.max_pages), _list("q_start", q_start, dev, n + 1),
-            _list("q_seq", q_seq, dev, nt), _list("positions", positions, dev, nt), _list("q_n", q_n, dev, nt),
-            _list("slots", slots, dev, nt), _list("kv_len", kv_len, dev, n),
-            _list("free_head_out", free_head_out, dev, 1), ws.data_ptr(), _bytes(ws, dev))
+            _list("seq_len", seq_len, dev, n, i32), _list("new_len", new_len, dev, n, i32),
+            _list("fork_src", fork_src, dev, n, i32), _list("free_pages", free_pages, dev, tp.n_free, i32),
+            _list("free_head", free_head, dev, 1, i32), _dense("page_table", page_table, dev, "i32", n, tp.max_pages),
+            _list("q_start", q_start, dev, n + 1, i32), _list("q_seq", q_seq, dev, nt, i32),
+            _list("positions", positions, dev, nt, i32), _list("q_n", q_n, dev, nt, i32),
+            _list("slots", slots, dev, nt, i32), _list("kv_len", kv_len, dev, n, i32),
+            _list("free_head_out", free_head_out, dev, 1, i32), ws.data_ptr(), _bytes(ws, dev))
 
 
 def make_rope_spec(*, rope_dim=64, layout=ROPE_INTERLEAVED, theta=10000.0, scaling=ROPE_SCALE_NONE, factor=1.0,
@@ -450,7 +454,7 @@ def _rope(fn, what, rs, rp, src, positions, dst, stream, backward):
     xp = _heads("dx" if backward else "x", x, dev, kind, nt, rp.x_heads, d, rp.x_token_stride, rp.x_head_stride)
     yp = _heads("dy" if backward else "y", y, dev, kind, nt, h, d, rp.y_token_stride, rp.y_head_stride)
     _launch(fn, what, dev, stream, ctypes.byref(rs), ctypes.byref(rp), yp if backward else xp,
-            _list("positions", positions, dev, nt), xp if backward else yp)
+            _list("positions", positions, dev, nt, _types("i32")), xp if backward else yp)
 
 
 def rope(rs, rp, x, positions, y, stream=None):
@@ -500,23 +504,23 @@ def _cache_rows(what, t, dev, kind, rows, row_stride):
 
 def latent_append(rs, c_kv, k_pe, positions, slots, kv_cache, ws, stream=None):
     """Append [c_kv | rope(k_pe)] rows to the bf16 latent cache [rows, >= 576]."""
-    nt, dev = slots.shape[0], _device("dsa_latent_append", slots)
+    nt, dev, i32 = slots.shape[0], _device("dsa_latent_append", slots), _types("i32")
     cache, stride = _cache("kv_cache", kv_cache, dev, "bf16")
     _launch(lib().dsa_latent_append, "dsa_latent_append", dev, stream, ctypes.byref(rs), nt,
             _part("c_kv", c_kv, dev, nt, 512), c_kv.stride(0), _part("k_pe", k_pe, dev, nt, 64), k_pe.stride(0),
-            _list("positions", positions, dev, nt), _list("slots", slots, dev, nt), cache, stride, kv_cache.shape[0],
-            ws.data_ptr(), _bytes(ws, dev))
+            _list("positions", positions, dev, nt, i32), _list("slots", slots, dev, nt, i32), cache, stride,
+            kv_cache.shape[0], ws.data_ptr(), _bytes(ws, dev))
 
 
 def latent_append_fp8(rs, c_kv, k_pe, positions, slots, kv8_cache, kv_scale, ws, stream=None):
     """The same into the FP8 latent cache [rows, >= 576] (e4m3 codes, power-of-two row scales)."""
-    nt, dev = slots.shape[0], _device("dsa_latent_append_fp8", slots)
+    nt, dev, i32 = slots.shape[0], _device("dsa_latent_append_fp8", slots), _types("i32")
     rows = kv8_cache.shape[0]
     cache, stride = _cache("kv8_cache", kv8_cache, dev, "e4m3")
     _launch(lib().dsa_latent_append_fp8, "dsa_latent_append_fp8", dev, stream, ctypes.byref(rs), nt,
             _part("c_kv", c_kv, dev, nt, 512), c_kv.stride(0), _part("k_pe", k_pe, dev, nt, 64), k_pe.stride(0),
-            _list("positions", positions, dev, nt), _list("slots", slots, dev, nt), cache, stride,
-            _list("kv_scale", kv_scale, dev, rows, "fp32"), rows, ws.data_ptr(), _bytes(ws, dev))
+            _list("positions", positions, dev, nt, i32), _list("slots", slots, dev, nt, i32), cache, stride,
+            _list("kv_scale", kv_scale, dev, rows, _types("fp32")), rows, ws.data_ptr(), _bytes(ws, dev))
 
 
 def shared_prefix_workspace_size(p: Params, kv: KV, ngroups: int) -> int:
@@ -529,9 +533,9 @@ def shared_prefix_workspace_size(p: Params, kv: KV, ngroups: int) -> int:
 def mla_shared_prefix(p, kv, ngroups, group_q0, group_n, q, kv_cache, kv_row_stride, out, lse, ws, stream=None):
     """Dense MLA attention of queries in groups that share a prefix, each
     prefix read once for the whole group."""
-    nq, h, dev = p.nq, p.h, _device("dsa_mla_shared_prefix", group_q0)
+    nq, h, dev, i32 = p.nq, p.h, _device("dsa_mla_shared_prefix", group_q0), _types("i32")
     _launch(lib().dsa_mla_shared_prefix, "dsa_mla_shared_prefix", dev, stream, ctypes.byref(p), ctypes.byref(kv),
-            ngroups, _list("group_q0", group_q0, dev, ngroups + 1), _list("group_n", group_n, dev, ngroups),
+            ngroups, _list("group_q0", group_q0, dev, ngroups + 1, i32), _list("group_n", group_n, dev, ngroups, i32),
             _dense("q", q, dev, "bf16", nq, h, 576),
             _cache_rows("kv_cache", kv_cache, dev, "bf16", kv.cache_rows, kv_row_stride), kv_row_stride,
             _dense("out", out, dev, "bf16", nq, h, 512), _dense("lse", lse, dev, "fp32", nq, h), ws.data_ptr(),
