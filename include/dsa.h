@@ -515,7 +515,8 @@ int dsa_rope_backward(const dsa_rope_spec *rs, const dsa_rope_params *rp, const 
  *   rs        rope_dim = 64 (the rope part of the 576-wide row)
  *   c_kv      [nt, 512] bf16, rows c_kv_stride elements apart;  k_pe [nt, 64]
  *             bf16, rows k_pe_stride apart (both 16-byte aligned, strides
- *             multiples of 8: they may be the two parts of one [nt, 576] array)
+ *             multiples of 8, ignored for one row: they may be the two parts
+ *             of one [nt, 576] array)
  *   positions [nt] int32;  slots [nt] int32 cache rows (dsa_build_tables);
  *             -1 is padding and writes nothing; a row outside [0, cache_rows)
  *             flags DSA_ERR_DEVICE_CHECK and is not written; a row listed

@@ -175,7 +175,7 @@ int append_common(const dsa_rope_spec *rs, int32_t nt, const void *c_kv, int64_t
         return fail(DSA_ERR_INVALID_ARG, "c_kv, k_pe and the cache must be 16-byte aligned");
     if (nt > 1 && (c_stride < kLatent || pe_stride < kRopeRow))
         return fail(DSA_ERR_INVALID_ARG, "rows of c_kv or k_pe overlap");
-    if (c_stride % 8 != 0 || pe_stride % 8 != 0) return fail(DSA_ERR_INVALID_ARG, "input strides must be multiples of 8");
+    if (nt > 1 && (c_stride % 8 != 0 || pe_stride % 8 != 0)) return fail(DSA_ERR_INVALID_ARG, "input strides must be multiples of 8");
     if (int frc = host_fault("append")) return frc;
     AppendParams a;
     memset(&a, 0, sizeof a);

@@ -202,3 +202,13 @@ def test_speeds_that_are_not_finite_are_refused(L, kw):
     assert rope(L, {"rope_dim": 64, **kw}) == dsa.DSA_ERR_INVALID_ARG
     if kw.get("rope_dim", 64) == 64:
         assert append(L, kw) == dsa.DSA_ERR_INVALID_ARG
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+def test_strides_of_a_single_row_are_not_looked_at(L, monkeypatch, fp8):
+    """One row has no neighbour: whatever stride a tensor of one row reports
+    passes the checks (the call then ends at the injected host failure)."""
+    monkeypatch.setenv("DSA_TEST_INJECT_HOST_ERROR", "append")
+    for cs, ps in ((1, 1), (0, 0), (577, 577), (-3, 5)):
+        assert append(L, nt=1, cs=cs, ps=ps, fp8=fp8) == dsa.DSA_ERR_CUDA
+        assert append(L, nt=2, cs=cs, ps=ps, fp8=fp8) == dsa.DSA_ERR_INVALID_ARG
