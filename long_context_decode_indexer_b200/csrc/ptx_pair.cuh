@@ -28,12 +28,21 @@ __device__ __forceinline__ uint32_t remote_smem(const void *p, uint32_t rank) {
     return r;
 }
 // Arrive on a barrier anywhere in the cluster (address from remote_smem).
-// What the arrival announces is read by the tensor cores of the arriving
-// thread's own SM (its shared memory, after a proxy fence) or has been read
-// already (TMEM), so the release is at CTA scope: at cluster scope it waits
-// for every memory operation of the thread, 1500 cycles a tile here.
+// The arrival itself orders nothing.  What was done to TMEM before it is
+// ordered by the tcgen05 fences on both sides; what was written to shared
+// memory by cluster_release_smem() before it and cluster_acquire_smem() behind
+// the other side's wait.
 __device__ __forceinline__ void cluster_arrive(uint32_t bar) {
-    asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+    asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+// Release and acquire at cluster scope for shared memory alone.  (A release of
+// everything waits for the thread's global stores too: 1500 cycles a tile in
+// k18.)
+__device__ __forceinline__ void cluster_release_smem() {
+    asm volatile("fence.release.sync_restrict::shared::cta.cluster;" ::: "memory");
+}
+__device__ __forceinline__ void cluster_acquire_smem() {
+    asm volatile("fence.acquire.sync_restrict::shared::cluster.cluster;" ::: "memory");
 }
 // Announce bytes that TMA loads will bring; orders nothing of this thread's
 // (a release at cluster scope here would wait for its memory operations).
@@ -53,6 +62,29 @@ __device__ __forceinline__ bool mbar_test(uint64_t *bar, uint32_t parity) {
         : "r"(smem_u32(bar)), "r"(parity)
         : "memory");
     return done != 0;
+}
+
+// The bounded wait for a barrier that the other CTA's threads arrive on.
+__device__ __forceinline__ bool mbar_wait_cluster(uint64_t *bar, uint32_t parity, long long budget) {
+    auto try_wait = [&]() {
+        uint32_t done;
+        asm volatile(
+            "{\n\t.reg .pred p;\n\t"
+            "mbarrier.try_wait.parity.relaxed.cluster.shared::cta.b64 p, [%1], %2;\n\t"
+            "selp.u32 %0, 1, 0, p;\n\t}"
+            : "=r"(done)
+            : "r"(smem_u32(bar)), "r"(parity)
+            : "memory");
+        return done != 0;
+    };
+    if (!try_wait()) {
+        const long long t0 = clock64();
+        while (!try_wait()) {
+            if (clock64() - t0 > budget) return false;
+        }
+    }
+    cluster_acquire_smem();
+    return true;
 }
 
 // Fetch a tensor map's descriptor ahead of its first load.

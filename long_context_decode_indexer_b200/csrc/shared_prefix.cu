@@ -526,7 +526,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPfxThreads, 1)
                             }
                             fence_proxy_async_smem();
                             __syncwarp();
-                            if (elect_one()) cluster_arrive(full0 + s * 8);
+                            if (elect_one()) {
+                                cluster_release_smem();
+                                cluster_arrive(full0 + s * 8);
+                            }
                         }
                         advance();
                     }
@@ -581,6 +584,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPfxThreads, 1)
             tc_fence_after();
             return w;
         };
+        // the same where the other CTA's threads have written
+        auto wait_peer = [&](uint64_t *bar, uint32_t parity) {
+            const bool w = __all_sync(0xffffffffu, mbar_wait_cluster(bar, parity, a.wait_budget) && !sm.abort) != 0;
+            tc_fence_after();
+            return w;
+        };
         bool ahead = false;  // the next stage has arrived (looked at one stage ahead)
         auto wait_full = [&]() {
             if (!__all_sync(0xffffffffu, ahead)) return wait(&sm.full[s], ph);
@@ -626,13 +635,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPfxThreads, 1)
                 // P(j) written (so S(j) read, and O rescaled); the first tile
                 // of a piece overwrites O, which the last piece's epilogue
                 // must have read
-                ok = wait(&sm.p_full, it & 1u);
-                if (ok && j == t0 && pieces > 0) ok = wait(&sm.o_empty, static_cast<uint32_t>(pieces - 1) & 1u);
+                ok = wait_peer(&sm.p_full, it & 1u);
+                if (ok && j == t0 && pieces > 0) ok = wait_peer(&sm.o_empty, static_cast<uint32_t>(pieces - 1) & 1u);
                 if (!ok) break;
                 const int groups = groups_of(t, j);
                 for (int g = 0; g < groups; ++g) {
+                    // a group with rows cleared by the loading warps themselves
+                    const int p = tile_start(t, j) + 64 * g;
+                    const bool edge = p < t.lo || p + 64 > t.hi;
                     for (int nh = 0; nh < 2; ++nh) {
-                        if (!(ok = wait_full())) break;
+                        if (!(ok = edge ? wait_peer(&sm.full[s], ph) : wait_full())) break;
                         if (elect_one()) {
                             const uint32_t d = tmem + kColO + nh * 128;
                             const uint64_t ad = p_desc + g * (kChunk / 16), bd = v_desc + s * (kStage / 16);
@@ -761,7 +773,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPfxThreads, 1)
                     fence_proxy_async_smem();
                     tc_fence_before();
                     __syncwarp();
-                    if (lane == 0 && !skip) cluster_arrive(p_full);
+                    if (lane == 0 && !skip) {
+                        cluster_release_smem();
+                        cluster_arrive(p_full);
+                    }
                     skip = false;
                 }
             }
