@@ -127,3 +127,40 @@ def test_angles_of_appended_rows(fp8):
         code = torch.from_numpy(want.astype(np.float32)).to(torch.float8_e4m3fn)
         assert torch.equal(cache[:, 512:].cpu().view(n, 32, 2), code.view(torch.uint8))
     assert dsa.check_status(ws) == dsa.DSA_OK
+
+
+# --------------------------------------------------- values that are not finite
+@pytest.mark.parametrize("dtype", [dsa.DTYPE_BF16, dsa.DTYPE_FP16, dsa.DTYPE_FP32])
+@pytest.mark.parametrize("layout", [0, 1])
+@pytest.mark.parametrize("xh,d,begin", [(6, 64, 0), (6, 70, 3), (1, 64, 0), (1, 70, 3)])
+@pytest.mark.parametrize("value", [float("nan"), float("inf"), float("-inf")])
+def test_values_that_are_not_finite_stay_in_their_pair(dtype, layout, xh, d, begin, value):
+    """They reach the two elements of their pair (every head's, where heads
+    share it; the shared gradient's pair, where heads are summed) and nothing
+    else; in a token that is padding they reach nothing."""
+    dt = {dsa.DTYPE_BF16: torch.bfloat16, dsa.DTYPE_FP16: torch.float16, dsa.DTYPE_FP32: torch.float32}[dtype]
+    nt, h, rot = 5, 6, 64
+    g = torch.Generator(device="cuda")
+    g.manual_seed(1)
+    rs = dsa.make_rope_spec(rope_dim=rot, layout=layout)
+    rp = dsa.make_rope_params(nt=nt, h=h, x_heads=xh, d=d, begin=begin, dtype=dtype)
+    p = torch.tensor([3, 1000, -1, 77, 12345], dtype=torch.int32, device="cuda")
+    pair = 9
+    i0, i1 = (begin + 2 * pair, begin + 2 * pair + 1) if layout == 0 else (begin + pair, begin + pair + rot // 2)
+    for backward in (False, True):
+        heads_in, heads_out = (h, xh) if backward else (xh, h)
+        x = torch.randn((nt, heads_in, d), generator=g, device="cuda").to(dt)
+        fn = dsa.rope_backward if backward else dsa.rope
+        want, got = (torch.zeros((nt, heads_out, d), dtype=dt, device="cuda") for _ in range(2))
+        fn(rs, rp, x, p, want)
+        x[1, heads_in - 1, i1] = value
+        x[2, 0, i0] = value                      # padding
+        if begin:
+            x[3, 0, begin - 1] = value           # copied, not turned
+        fn(rs, rp, x, p, got)
+        touched = torch.zeros((nt, heads_out, d), dtype=torch.bool, device="cuda")
+        touched[1, slice(None) if xh == 1 else h - 1, [i0, i1]] = True
+        if begin:
+            touched[3, slice(None) if xh == 1 else 0, begin - 1] = True
+        assert torch.equal(got[~touched], want[~touched])
+        assert not torch.isfinite(got[touched]).any()
