@@ -62,6 +62,7 @@ struct MhaSmem {
     uint64_t p_full[2];
     uint64_t pv_done[2];
     uint64_t mma_done;
+    uint64_t v_edge;
     uint32_t tmem_base;
     volatile int32_t abort;
     int32_t n_max;
@@ -133,6 +134,7 @@ __global__ void __launch_bounds__(kMhaThreads, 1)
             mbar_init(&sm.pv_done[b], 1);
         }
         mbar_init(&sm.mma_done, 1);
+        mbar_init(&sm.v_edge, 1);
         fence_mbar_init();
     }
     if (warp == 1) {
@@ -164,13 +166,17 @@ __global__ void __launch_bounds__(kMhaThreads, 1)
 
     if (warp == 0) {
         // ------------------------------------------------ TMA producer
+        // rows of the last tile behind every history may hold anything: their
+        // weights are 0, and 0 * NaN is NaN, so they are cleared before the
+        // MMA reads them
+        const int v_rows = sm.n_max - (nkt - 1) * kMhaTile;  // of the last tile
+        int k_end = 0, v_end = 0;  // tiles whose K / V loads were issued
         if (lane == 0 && nkt > 0) {
             mbar_arrive_expect_tx(&sm.q_full, static_cast<uint32_t>(QC) * kChunkBytes);
             for (int c = 0; c < QC; ++c)
                 tma_load_3d(base + L.q + c * kChunkBytes, &qmap, &sm.q_full, c * 64, head, t0);
             // K(j) and V(j) in order; a K slot frees once S(j) is computed,
             // a V slot once P(j) . V(j) is, so K runs ahead of V
-            int k_end = 0, v_end = 0;  // tiles whose K / V loads were issued
             for (int j = 0; j < nkt; ++j) {
                 const int ks = j % a.stages, vs = j % kMhaVStages;
                 const int r = static_cast<int>(row0) + j * kMhaTile;
@@ -191,12 +197,30 @@ __global__ void __launch_bounds__(kMhaThreads, 1)
                     sm.abort = 1;
                     break;
                 }
-                mbar_arrive_expect_tx(&sm.v_full[vs], L.v_stage);
+                uint64_t *v_bar = j == nkt - 1 && v_rows < kMhaTile ? &sm.v_edge : &sm.v_full[vs];
+                mbar_arrive_expect_tx(v_bar, L.v_stage);
                 for (int c = 0; c < VC; ++c)
-                    tma_load_3d(base + L.v_ring + vs * L.v_stage + c * kChunkBytes, &vmap, &sm.v_full[vs], c * 64,
-                                head, r);
+                    tma_load_3d(base + L.v_ring + vs * L.v_stage + c * kChunkBytes, &vmap, v_bar, c * 64, head, r);
                 v_end = j + 1;
             }
+        }
+        v_end = __shfl_sync(0xffffffffu, v_end, 0);
+        if (nkt > 0 && v_end == nkt && v_rows < kMhaTile) {
+            const int vs = (nkt - 1) % kMhaVStages;
+            if (__all_sync(0xffffffffu, mbar_wait(&sm.v_edge, 0, a.wait_budget))) {
+                for (int c = 0; c < VC; ++c) {
+                    uint4 *dst = reinterpret_cast<uint4 *>(base + L.v_ring + vs * L.v_stage + c * kChunkBytes);
+                    for (int i = v_rows * 8 + lane; i < kMhaTile * 8; i += 32) dst[i] = make_uint4(0u, 0u, 0u, 0u);
+                }
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&sm.v_full[vs]);
+            } else if (lane == 0) {
+                record_status(a.status, DSA_ERR_TIMEOUT);
+                sm.abort = 1;
+            }
+        }
+        if (lane == 0 && nkt > 0) {
             // every load issued lands before the CTA may exit (a no-op when
             // the MMAs consumed them all)
             mbar_wait(&sm.q_full, 0, a.wait_budget);

@@ -108,3 +108,44 @@ def test_entries_that_are_not_visible_stay_out():
     ref, rl, mag, _ = attention(q[0].double(), kv_c[1:41].double(), SCALE)
     assert torch.all((out[0].double() - ref).abs() <= 2.0 ** -8 * ref.abs() + 2.0 ** -10 * ref.abs().amax() + 2.0 ** -13 * mag)
     assert not out[1].any() and torch.all(torch.isneginf(lse[1]))
+
+
+@pytest.mark.parametrize("fill", [float("nan"), float("inf")])
+@pytest.mark.parametrize("d_qk,d_v", [(192, 128), (64, 64)])
+@pytest.mark.parametrize("lengths", [[1], [100, 128, 129], [300], [16, 383]])
+def test_masked_mha_of_rows_behind_the_sequences(fill, d_qk, d_v, lengths):
+    """Sequences of one length each, apart in k and v; the rows between and
+    behind them are nobody's."""
+    L, h, gap = max(lengths), 3, 200
+    nq, rows = L * len(lengths), (L + gap) * len(lengths)
+    g = torch.Generator(device="cuda")
+    g.manual_seed(L)
+    q = torch.randn((nq, h, d_qk), generator=g, device="cuda").bfloat16()
+    k, v = (torch.randn((rows, h, d), generator=g, device="cuda").bfloat16() for d in (d_qk, d_v))
+    row0 = np.arange(len(lengths)) * (L + gap)
+    n = np.concatenate([np.minimum(np.arange(1, L + 1), x) for x in lengths])
+    used = np.zeros(rows, bool)
+    for r, x in zip(row0, lengths):
+        used[r:r + x] = True
+    used = torch.from_numpy(used).cuda()
+    p = dsa.make_params(nq=nq, h_idx=1, d_idx=64, h=h, topk=1, max_n=L, q_per_seq=L, scale=d_qk ** -0.5, d_qk=d_qk, d_v=d_v)
+    keep = [_i32(np.repeat(np.arange(len(lengths)), L)), _i32(n), torch.from_numpy(row0).cuda()]
+    kv = dsa.make_kv(q_seq=keep[0], q_n=keep[1], seq_row0=keep[2], cache_rows=rows)
+    ws = workspace(dsa.workspace_size(p, kv, dsa.OP_MASKED_MHA))
+    got = []
+    for bad in (0.0, fill):
+        k[~used], v[~used] = bad, bad
+        out = torch.full((nq, h, d_v), 5.0, dtype=torch.bfloat16, device="cuda")
+        lse = torch.full((nq, h), 5.0, device="cuda")
+        dsa.masked_mha_prefill(p, kv, q, k, v, None, out, lse, ws)
+        assert dsa.check_status(ws) == dsa.DSA_OK
+        got.append((out, lse))
+    assert torch.equal(got[0][0].view(torch.int16), got[1][0].view(torch.int16)) and torch.equal(got[0][1], got[1][1])
+    for t in (0, L - 1, nq - 1):
+        b, m = t // L, int(n[t])
+        kk, vv = (x[row0[b]:row0[b] + m].double().transpose(0, 1) for x in (k, v))
+        s = torch.einsum("hd,hsd->hs", q[t].double(), kk) * d_qk ** -0.5
+        ref = torch.einsum("hs,hsd->hd", torch.softmax(s, 1), vv)
+        mag = torch.einsum("hs,hsd->hd", torch.softmax(s, 1), vv.abs())
+        # bf16 output; P as a bf16 pair and fp32 sums 2^-13 of the magnitudes
+        assert torch.all((got[1][0][t].double() - ref).abs() <= 2.0 ** -8 * ref.abs() + 2.0 ** -13 * mag)
