@@ -114,6 +114,13 @@ __device__ __forceinline__ bool bar_and(int id, int count, bool pred) {
     return r != 0;
 }
 
+// 16-byte global -> shared copy where `read` (cp.async, completion by group),
+// else 16 zero bytes (nothing is read).
+__device__ __forceinline__ void cp_async16_or_zero(void *dst, const void *src, bool read) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_u32(dst)), "l"(src), "r"(read ? 16u : 0u)
+                 : "memory");
+}
+
 __device__ __forceinline__ uint32_t pack_half2(float lo, float hi) {
     const uint32_t a = __half_as_ushort(__float2half_rn(lo));
     const uint32_t b = __half_as_ushort(__float2half_rn(hi));
