@@ -17,6 +17,7 @@
 #include <math.h>
 #include <stdint.h>
 
+#include "api_util.h"
 #include "dsa.h"
 #include "ptx.cuh"
 #include "serving.h"
@@ -346,7 +347,7 @@ cudaError_t launch_rope_t(RopeParams a, int shared, cudaStream_t st) {
         a.hp = kRopeThreads / a.units < 1 ? 1 : (kRopeThreads / a.units > a.h ? a.h : kRopeThreads / a.units);
         // few threads a unit where there are many tokens (4, 8, 32: 29, 31, 45
         // us for 8191 x 128 x 64 bf16), many where there are few
-        const int most = static_cast<int64_t>(a.nt) * a.units < 148 * kRopeThreads / 8 ? 32 : 4;
+        const int most = static_cast<int64_t>(a.nt) * a.units < num_sms() * kRopeThreads / 8 ? 32 : 4;
         if (a.hp > most) a.hp = most;
         a.tp = kRopeThreads / (a.units * a.hp) < 1 ? 1 : kRopeThreads / (a.units * a.hp);
         const int64_t grid = (static_cast<int64_t>(a.nt) + a.tp - 1) / a.tp;
@@ -384,7 +385,7 @@ cudaError_t launch_rope_t(RopeParams a, int shared, cudaStream_t st) {
     const int64_t gx = (static_cast<int64_t>(a.nt) + a.tp - 1) / a.tp;
     int iters = (a.h + a.hp - 1) / a.hp;  // fewer than four heads while the grid is small
     if (iters > 4) iters = 4;
-    while (iters > 1 && gx * gz * ((a.h + a.hp * iters - 1) / (a.hp * iters)) < 148 * 4) iters = (iters + 1) / 2;
+    while (iters > 1 && gx * gz * ((a.h + a.hp * iters - 1) / (a.hp * iters)) < num_sms() * 4) iters = (iters + 1) / 2;
     a.iters = iters;
     const dim3 grid(static_cast<unsigned>(gx), static_cast<unsigned>((a.h + a.hp * iters - 1) / (a.hp * iters)), gz);
     const int threads = a.ub * a.hp * a.tp;
