@@ -164,3 +164,28 @@ def test_values_that_are_not_finite_stay_in_their_pair(dtype, layout, xh, d, beg
             touched[3, slice(None) if xh == 1 else 0, begin - 1] = True
         assert torch.equal(got[~touched], want[~touched])
         assert not torch.isfinite(got[touched]).any()
+
+
+@pytest.mark.parametrize("layout", [0, 1])
+@pytest.mark.parametrize("h,xh,d,begin", [(6, 6, 64, 0), (6, 1, 64, 0), (6, 6, 70, 3), (6, 1, 70, 3), (1, 1, 70, 3)])
+def test_sources_that_repeat_a_row(layout, h, xh, d, begin):
+    """Strides of 0 on the side that is read (an expanded row, the gradient
+    of a sum): the same bits as with the rows written out."""
+    nt = 21
+    p = torch.arange(-1, nt - 1, dtype=torch.int32, device="cuda") * 97
+    rs = dsa.make_rope_spec(layout=layout)
+    g = torch.Generator(device="cuda")
+    g.manual_seed(2)
+    for backward in (False, True):
+        heads_in, heads_out = (h, xh) if backward else (xh, h)
+        for row in ((1, heads_in, d), (nt, 1, d), (1, 1, d)):
+            x = torch.randn(row, generator=g, device="cuda").expand(nt, heads_in, d)
+            st = x.stride()[:2]
+            got = []
+            for src in (x, x.contiguous()):
+                kw = {} if src is not x else ({"y_strides": st} if backward else {"x_strides": st})
+                rp = dsa.make_rope_params(nt=nt, h=h, x_heads=xh, d=d, begin=begin, dtype=dsa.DTYPE_FP32, **kw)
+                dst = torch.full((nt, heads_out, d), 7.0, device="cuda")
+                (dsa.rope_backward if backward else dsa.rope)(rs, rp, src, p, dst)
+                got.append(dst)
+            assert torch.equal(got[0], got[1])

@@ -185,3 +185,19 @@ def test_the_error_of_a_whole_output(temp):
         err += float((e * e).sum())
         want += float((step * step).sum()) / 12 + 2.0 ** -14 / 12 * 0.541 * float((rms * rms).sum())
     assert err <= 1.3 * want, "square error %.3g of what is predicted" % (err / want)
+
+
+@pytest.mark.parametrize("page", [0, 64])
+def test_groups_without_queries(page):
+    """Groups of no queries before, between and behind the others, more
+    groups than queries."""
+    c = Chunks([(300, [(300, 2)]), (70, [(90, 1), (70, 1)])], 16, page, seed=8)
+    clean, clean_l = c.run()
+    q0, n = c.keep[4].tolist(), c.keep[5].tolist()
+    c.keep[4] = _i32([0, 0, 0, q0[1], q0[1], q0[1], q0[2], q0[2], q0[2]])
+    c.keep[5] = _i32([5, 300, n[0], 0, 299, n[1], 64, 1])
+    c.ng = 8
+    c.ws = workspace(dsa.shared_prefix_workspace_size(c.p, c.kvd, 8))
+    out, lse = c.run()
+    c.check(out, lse, range(4))
+    assert torch.equal(out, clean) and torch.equal(lse, clean_l)
