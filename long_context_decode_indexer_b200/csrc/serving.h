@@ -32,13 +32,18 @@ inline cudaError_t launch_dependent(void (*kern)(KArgs...), int grid, int block,
 constexpr int kTabThreads = 512;
 constexpr int kTabMaxSeq = 16384;  // three int32 per sequence in shared memory: 192 KB
 
+// kv_len is seq_len, or free_head_out is free_head: written behind a barrier of
+// the cluster that is the whole grid, or by a second kernel.
+enum { kTabApart = 0, kTabAdvanceCluster = 1, kTabAdvanceLater = 2 };
+constexpr int kTabCluster = 8;
+
 struct TableParams {
     const int32_t *seq_len, *new_len, *fork_src, *free_pages, *free_head;
     int32_t *page_table, *q_start, *q_seq, *positions, *q_n, *slots, *kv_len, *free_head_out;
     int32_t nseq, nt, page_size, max_pages, n_free, sees_self;
     int32_t page_shift;  // page_size = 1 << page_shift, or -1
     int32_t vec;         // the token arrays are 16-byte aligned
-    int32_t in_place;    // kv_len is seq_len, or free_head_out is free_head
+    int32_t in_place;    // kTabApart, or how lengths and head are advanced in place
     int64_t n_pages;     // page ids are 0..n_pages-1
     int32_t *taken;      // ws: pages handed out, from k13 to k13_advance (in place)
     int *status;

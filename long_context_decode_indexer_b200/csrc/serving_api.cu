@@ -293,7 +293,6 @@ int dsa_build_tables(const dsa_table_params *tp, const int32_t *seq_len, const i
     for (int i = 0; i <= 16; ++i)
         if (tp->page_size == 1 << i) a.page_shift = i;
     a.vec = aligned(q_seq, 16) && aligned(positions, 16) && aligned(q_n, 16) && aligned(slots, 16);
-    a.in_place = kv_len == seq_len || free_head_out == free_head;
     a.n_pages = tp->cache_rows / tp->page_size;
     a.status = at<int>(ws, 0);
     a.taken = at<int32_t>(ws, 256);
@@ -301,6 +300,15 @@ int dsa_build_tables(const dsa_table_params *tp, const int32_t *seq_len, const i
     const int by_tokens = (tp->nt + 4 * kTabThreads - 1) / (4 * kTabThreads), by_seqs = (tp->nseq + 63) / 64;
     int grid = by_tokens > by_seqs ? by_tokens : by_seqs;
     grid = grid < 1 ? 1 : (grid > num_sms() ? num_sms() : grid);
+    if (kv_len == seq_len || free_head_out == free_head) {
+        a.in_place = grid <= kTabCluster ? kTabAdvanceCluster : kTabAdvanceLater;
+        if (grid <= kTabCluster)
+            for (int g = 1; g < 2 * kTabCluster; g *= 2)  // a cluster of 1, 2, 4 or 8
+                if (g >= grid) {
+                    grid = g;
+                    break;
+                }
+    }
     cudaError_t e = launch_build_tables(a, grid, static_cast<cudaStream_t>(stream));
     if (e != cudaSuccess) return cuda_fail(e, "page table launch");
     return DSA_OK;

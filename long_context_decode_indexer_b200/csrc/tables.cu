@@ -13,10 +13,12 @@
 // scan), then takes its share of the tokens (each finds its sequence by a
 // binary search in shared memory) and of the sequences (one warp each, for
 // the table entries).  Nothing a CTA reads is written by another.  Where the
-// new lengths or the new head replace the old ones, a small second kernel
-// writes them once every CTA has read the old ones (a counter of finished
-// CTAs would do without it, but would rely on what earlier calls left in the
-// workspace).  What bounds it is the chain of dependent loads: lengths,
+// new lengths or the new head replace the old ones, every CTA has to have read
+// them first: up to eight CTAs are one cluster and meet at its barrier (128
+// idle sequences: 3.6 us apart, 4.25 in place, 4.7 with a second kernel); more
+// leave it to a small second kernel (4096: 6.2 and 7.5 us).  A counter of
+// finished CTAs (4.3 and 7.6 us) would rely on what earlier calls left in the
+// workspace.  What bounds it is the chain of dependent loads: lengths,
 // shared-memory search, page (4.5 us for 128 sequences of two tokens, 10.8 us
 // for 4096 sequences and 100000 tokens).
 #include <cuda_runtime.h>
@@ -24,6 +26,7 @@
 
 #include "dsa.h"
 #include "ptx.cuh"
+#include "ptx_pair.cuh"
 #include "serving.h"
 
 namespace dsa {
@@ -201,17 +204,9 @@ __global__ void __launch_bounds__(kTabThreads, 1) k13_build_tables(const TablePa
                 }
         }
     }
-    // ---- sequences: offsets, lengths, then table entries
-    for (int b = gtid; b < a.nseq; b += gthreads) {
-        a.q_start[b] = refuse ? 0 : tok0[b];
-        if (!a.in_place) a.kv_len[b] = refuse ? a.seq_len[b] : len[b] + (tok0[b + 1] - tok0[b]);
-    }
-    if (gtid == 0) {
-        const int32_t taken = refuse ? 0 : static_cast<int32_t>(total_p);
-        a.q_start[a.nseq] = ntok;
-        if (a.in_place) *a.taken = taken;
-        else *a.free_head_out = head + taken;
-    }
+    // ---- sequences: offsets, table entries, lengths
+    for (int b = gtid; b < a.nseq; b += gthreads) a.q_start[b] = refuse ? 0 : tok0[b];
+    if (gtid == 0) a.q_start[a.nseq] = ntok;
     if (!refuse)
         for (int b = gtid >> 5; b < a.nseq; b += gthreads >> 5) {
             const int held = pages_of(len[b] + ps - 1), need = page0[b + 1] - page0[b];
@@ -222,6 +217,18 @@ __global__ void __launch_bounds__(kTabThreads, 1) k13_build_tables(const TablePa
             copy_entries(row + held, a.free_pages + head + page0[b], need, lane,
                          [&](int p) { return p >= 0 && p < a.n_pages ? p : -1; });
         }
+    const int32_t taken = refuse ? 0 : static_cast<int32_t>(total_p);
+    if (a.in_place == kTabAdvanceLater) {
+        if (gtid == 0) *a.taken = taken;
+        return;
+    }
+    if (a.in_place == kTabAdvanceCluster) {
+        __syncthreads();
+        cluster_sync_all();
+    }
+    for (int b = gtid; b < a.nseq; b += gthreads)
+        a.kv_len[b] = refuse ? a.seq_len[b] : len[b] + (tok0[b + 1] - tok0[b]);
+    if (gtid == 0) *a.free_head_out = head + taken;
 }
 
 // The lengths and the head in place, after k13: a refused batch has offsets
@@ -240,9 +247,20 @@ cudaError_t launch_build_tables(const TableParams &a, int grid, cudaStream_t st)
                                              (kTabMaxSeq + 1) * 12);
         if (e != cudaSuccess) return e;
     }
-    k13_build_tables<<<grid, kTabThreads, smem, st>>>(a);
-    cudaError_t e = cudaGetLastError();
-    if (e != cudaSuccess || !a.in_place) return e;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(grid);
+    cfg.blockDim = dim3(kTabThreads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = st;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = grid;
+    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = a.in_place == kTabAdvanceCluster ? 1 : 0;
+    cudaError_t e = cudaLaunchKernelEx(&cfg, k13_build_tables, a);
+    if (e == cudaSuccess) e = cudaGetLastError();
+    if (e != cudaSuccess || a.in_place != kTabAdvanceLater) return e;
     return launch_dependent(k13_advance, a.nseq > 0 ? (a.nseq + kTabThreads - 1) / kTabThreads : 1, kTabThreads, 0, st, a);
 }
 

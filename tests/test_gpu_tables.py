@@ -255,3 +255,18 @@ def test_in_place_on_a_workspace_that_another_call_wrote(alias, fill):
     s2.ws[dsa.WS_STATUS_BYTES:] = fill
     s2.call()
     assert s2.check() is None
+
+
+@pytest.mark.parametrize("n", [1, 60, 65, 130, 200, 300, 500, 512, 513, 2000])
+def test_in_place_at_every_grid(n):
+    """One CTA, clusters of up to eight, more than eight."""
+    rng = np.random.default_rng(n)
+    seq, new, fork, free, table, n_pages = _batch(rng, n, 64, 300, 0, 40)
+    s = Step(seq, new, free, table, int(new.sum()) + 1, 64, n_pages, alias=True)
+    s.ws[dsa.WS_STATUS_BYTES:] = 0x55
+    s.call()
+    assert s.check() is not None
+    s2 = Step(seq, new, free[:0], table, int(new.sum()) + 1, 64, n_pages, alias=True)   # no page to give
+    if (-(-(seq + new) // 64)).sum() > (-(-seq // 64)).sum():
+        s2.call()
+        assert s2.check() is None
