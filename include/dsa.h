@@ -520,7 +520,9 @@ int dsa_rope_backward(const dsa_rope_spec *rs, const dsa_rope_params *rp, const 
  *   positions [nt] int32;  slots [nt] int32 cache rows (dsa_build_tables);
  *             -1 is padding and writes nothing; a row outside [0, cache_rows)
  *             flags DSA_ERR_DEVICE_CHECK and is not written; a row listed
- *             twice ends up with elements of either token
+ *             twice is of no use afterwards (it ends up with elements of
+ *             either token, in FP8 with codes and a scale that need not belong
+ *             together)
  *   kv_cache  bf16 rows kv_row_stride elements apart (as for the attention)
  *   ws        DSA_WS_STATUS_BYTES
  * The rotation is computed in fp32 and rounded to bf16 once. */
@@ -533,14 +535,17 @@ int dsa_latent_append(const dsa_rope_spec *rs, int32_t nt, const void *c_kv, int
  * 576 values (rope part rotated in 64 bits) as e4m3 codes (ties to even) of
  * value / s, s = kv_scale[slot] the smallest power of two with amax / s <= 448
  * (at least 2^-126; 1 for a row of zeros).  Infinities and NaN do not enter
- * amax; an infinity is stored as +-448 s, NaN as NaN.  kv8_row_bytes and
- * kv_scale as for dsa_sparse_mla_decode_fp8. */
+ * amax; an infinity is stored as +-448 s, NaN as NaN, and a rotated value past
+ * the largest fp32 number counts as an infinity.  kv8_row_bytes and kv_scale as
+ * for dsa_sparse_mla_decode_fp8. */
 int dsa_latent_append_fp8(const dsa_rope_spec *rs, int32_t nt, const void *c_kv, int64_t c_kv_stride,
                           const void *k_pe, int64_t k_pe_stride, const int32_t *positions,
                           const int32_t *slots, void *kv8_cache, int64_t kv8_row_bytes, float *kv_scale,
                           int64_t cache_rows, void *ws, size_t ws_bytes, void *stream);
 
-/* Bytes of `ws` dsa_mla_shared_prefix needs for this shape (host only). */
+/* Bytes of `ws` dsa_mla_shared_prefix needs for this shape (host only): about
+ * 263 KB for every 128 (query, head) rows, for every group and for every query
+ * (2.2 GB for 4096 queries of 128 heads, 1.1 GB for 4096 of one head). */
 int dsa_shared_prefix_workspace_size(const dsa_params *p, const dsa_kv *kv, int32_t ngroups, size_t *bytes);
 
 /* Dense MQA-mode MLA attention of a batch whose queries share long prefixes,
@@ -562,8 +567,10 @@ int dsa_shared_prefix_workspace_size(const dsa_params *p, const dsa_kv *kv, int3
  * own sequence q_seq[i] behind it.  n may be less than group_n[g] (the query
  * then sees the first n shared positions) and 0 (out = 0, lse = -inf).  Rows
  * at or behind n are not used, whatever they hold.
- *   p      nq <= 4096, h, max_n, scale as elsewhere; the other fields are
- *          checked, not used
+ *   p      nq <= 4096 (a longer step, a prompt of 8192 tokens, goes in several
+ *          calls: a query's result does not depend on the others of its call
+ *          but for the order of its sums), h, max_n, scale as elsewhere; the
+ *          other fields are checked, not used
  *   kv     as for dsa_sparse_mla_decode (contiguous: seq_row0[b] + s may be
  *          outside the cache for shared positions of later sequences)
  *   ngroups 1..4096 (any number when nq = 0)

@@ -149,3 +149,52 @@ def test_masked_mha_of_rows_behind_the_sequences(fill, d_qk, d_v, lengths):
         mag = torch.einsum("hs,hsd->hd", torch.softmax(s, 1), vv.abs())
         # bf16 output; P as a bf16 pair and fp32 sums 2^-13 of the magnitudes
         assert torch.all((got[1][0][t].double() - ref).abs() <= 2.0 ** -8 * ref.abs() + 2.0 ** -13 * mag)
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+def test_a_served_cache_that_was_never_cleared(fp8):
+    """Tables, append and sparse attention over a cache that starts as NaN:
+    page 0 is never handed out, the lists are longer than the histories."""
+    rng = np.random.default_rng(0)
+    nseq, h, topk, rows = 3, 16, 256, 12 * 64
+    new = np.array([100, 1, 64])
+    nt = int(new.sum()) + 4
+    z = lambda n: torch.zeros(n, dtype=torch.int32, device="cuda")
+    seq, head, table = z(nseq), z(1), _i32(np.full((nseq, 4), -1))
+    q_start, q_seq, pos, q_n, slots = z(nseq + 1), z(nt), z(nt), z(nt), z(nt)
+    tp = dsa.make_table_params(nseq=nseq, nt=nt, page_size=64, max_pages=4, n_free=11, cache_rows=rows)
+    ws = workspace(dsa.table_workspace_size(tp))
+    dsa.build_tables(tp, seq, _i32(new), None, _i32(rng.permutation(np.arange(1, 12))), head, table, q_start, q_seq, pos,
+                     q_n, slots, seq, head, ws)
+    kv_a = torch.from_numpy(rng.standard_normal((nt, 576))).bfloat16().cuda()
+    rs = dsa.make_rope_spec()
+    if fp8:
+        cache = torch.full((rows, 576), 0x7F, dtype=torch.uint8, device="cuda")
+        sc = torch.full((rows,), float("nan"), device="cuda")
+        dsa.latent_append_fp8(rs, kv_a[:, :512], kv_a[:, 512:], pos, slots, cache, sc, ws)
+        values = cache.view(torch.float8_e4m3fn).double() * sc.double()[:, None]
+    else:
+        cache = torch.full((rows, 576), float("nan"), dtype=torch.bfloat16, device="cuda")
+        dsa.latent_append(rs, kv_a[:, :512], kv_a[:, 512:], pos, slots, cache, ws)
+        values = cache.double()
+    idx = np.full((nseq, topk), -1)
+    for b in range(nseq):
+        idx[b, :new[b]] = np.arange(new[b])
+    last = (q_start[1:] - 1).long()
+    q = torch.from_numpy(rng.standard_normal((nseq, h, 576))).bfloat16().cuda()
+    qs, qn = q_seq[last].contiguous(), q_n[last].contiguous()
+    p = dsa.make_params(nq=nseq, h_idx=4, d_idx=128, h=h, topk=topk, max_n=256, scale=SCALE)
+    kv = dsa.make_kv(q_seq=qs, q_n=qn, page_table=table, page_size=64, cache_rows=rows)
+    ws_m = workspace(dsa.workspace_size(p, kv, dsa.OP_SPARSE_MLA_DECODE))
+    out, lse = torch.zeros((nseq, h, 512), dtype=torch.bfloat16, device="cuda"), torch.zeros((nseq, h), device="cuda")
+    if fp8:
+        dsa.sparse_mla_decode_fp8(p, kv, q, cache, 576, sc, _i32(idx), out, lse, ws_m)
+    else:
+        dsa.sparse_mla_decode(p, kv, q, cache, 576, _i32(idx), out, lse, ws_m)
+    assert dsa.check_status(ws) == dsa.check_status(ws_m) == dsa.DSA_OK
+    for b in range(nseq):
+        at = slots[int(q_start[b]):int(q_start[b + 1])].long()
+        ref, rl, mag, _ = attention(q[b].double(), values[at], SCALE)
+        err = (out[b].double() - ref).abs()
+        assert torch.all(err <= 2.0 ** -8 * ref.abs() + 2.0 ** -10 * ref.abs().amax() + 2.0 ** -13 * mag)
+        assert float((lse[b].double() - rl).abs().max()) <= 1e-3
