@@ -389,32 +389,43 @@ def _list(what, t, dev, n, kinds):
     _refuse(what, "%d adjacent %s" % (n, "/".join(sorted(str(k) for k in kinds))), t, dev)
 
 
+def _joined(shape, strides, dims):
+    """How many steps the first `dims` dimensions are together, and how far
+    apart they lie (0 for one); None where they are not evenly spaced."""
+    n, step = 1, 0
+    for k in range(dims - 1, -1, -1):
+        if shape[k] == 1:
+            continue
+        if n == 1:
+            step = strides[k]
+        elif strides[k] != n * step:
+            return None
+        n *= shape[k]
+    return n, step
+
+
 def _heads(what, t, dev, kind, nt, heads, d, ts, hs):
     """The address of the rows [nt, heads, d] whose tokens are `ts` and heads
-    `hs` elements apart.  `t` is that view itself (or more tokens of it), the
-    same with heads and elements joined, [.., heads * d], or a flat buffer."""
+    `hs` elements apart.  `t` is that view itself (tokens in one dimension or
+    several, perhaps more of them), the same with heads and elements joined,
+    [.., heads * d], or a flat buffer."""
     if t.get_device() == dev and t.dtype in _types(kind):
         shape = t.shape
-        if shape == (nt, heads, d) and hs == d and ts == heads * d and t.is_contiguous():
+        if nt == 0 or shape == (nt, heads, d) and hs == d and ts == heads * d and t.is_contiguous():
             return t.data_ptr()   # the usual call
         strides = t.stride()
-        if nt == 0:
+        ends = len(shape) > 0 and (strides[-1] == 1 or shape[-1] == 1)
+        dims = -1     # of the tokens
+        if ends and shape[-2:] == (heads, d) and (heads == 1 or strides[-2] == hs):
+            dims = len(shape) - 2
+        elif ends and shape[-1] == heads * d and (heads == 1 or hs == d):
+            dims = len(shape) - 1
+        if dims >= 0:
+            tokens = _joined(shape, strides, dims)
+            if tokens and (tokens[0] == nt or dims == 1 and tokens[0] > nt) and (nt == 1 or tokens[1] == ts):
+                return t.data_ptr()
+        if ends and len(shape) == 1 and shape[0] >= (nt - 1) * ts + (heads - 1) * hs + d:
             return t.data_ptr()
-        if len(shape) == 3 and shape[1] == heads and shape[2] == d:
-            if shape[0] >= nt and (nt == 1 or strides[0] == ts) and (heads == 1 or strides[1] == hs) and \
-                    (d == 1 or strides[2] == 1):
-                return t.data_ptr()
-        elif len(shape) == 2 and shape[1] == heads * d:
-            if shape[0] >= nt and (nt == 1 or strides[0] == ts) and (heads == 1 or hs == d) and \
-                    (shape[1] == 1 or strides[1] == 1):
-                return t.data_ptr()
-        elif t.is_contiguous():
-            if len(shape) == 1:
-                if t.numel() >= (nt - 1) * ts + (heads - 1) * hs + d:
-                    return t.data_ptr()
-            elif t.numel() == nt * heads * d and (nt == 1 or ts == heads * d) and (heads == 1 or hs == d) and \
-                    (shape[-1] == heads * d or shape[-2:] == (heads, d)):
-                return t.data_ptr()
     _refuse(what, "%s rows [%d, %d, %d] of strides (%d, %d, 1)" % (("bf16", "fp16", "fp32")[kind], nt, heads, d, ts, hs), t, dev)
 
 
@@ -486,8 +497,8 @@ def _cache(what, t, dev, kind):
 
 def _cache_rows(what, t, dev, kind, rows, row_stride):
     """The address of a latent cache of `rows` rows, `row_stride` elements
-    apart: rows [rows, >= 576], pages [pages, page_size, >= 576] that lie one
-    behind the other, or a flat buffer (or an address)."""
+    apart: [.., >= 576] (rows, or pages of rows one behind the other), or a
+    flat buffer (or an address)."""
     if t is None or isinstance(t, int):
         return t
     if t.get_device() == dev and t.dtype in _types(kind):
@@ -495,9 +506,9 @@ def _cache_rows(what, t, dev, kind, rows, row_stride):
         if len(shape) == 1:
             if strides[0] == 1 and shape[0] >= (rows - 1) * row_stride + 576:
                 return t.data_ptr()
-        elif shape[-1] >= 576 and strides[-1] == 1 and strides[-2] == row_stride:
-            if len(shape) == 2 and shape[0] >= rows or \
-                    len(shape) == 3 and shape[0] * shape[1] >= rows and strides[0] == shape[1] * row_stride:
+        elif len(shape) > 1 and shape[-1] >= 576 and strides[-1] == 1:
+            n = _joined(shape, strides, len(shape) - 1)
+            if n and n[0] >= rows and (n[0] == 1 or n[1] == row_stride):
                 return t.data_ptr()
     _refuse(what, "%s, %d rows of >= 576 elements, %d apart," % (kind, rows, row_stride), t, dev)
 

@@ -278,3 +278,34 @@ def test_shared_prefix_of_no_queries_needs_no_tensors(calls):
     p = dsa.make_params(nq=0, h_idx=64, d_idx=128, h=16, topk=1, max_n=4096, scale=0.04)
     dsa.mla_shared_prefix(p, kv, 0, on(1), None, None, None, 576, None, None, a["ws"], stream=0)
     assert calls.pop()[1][5:8] == (None, None, 576)
+
+
+def test_views_of_several_token_or_page_dimensions(calls):
+    """[batch, length, heads, width] and its slices, [pages, size, 1, width]:
+    evenly spaced rows are what they are, whatever they are called."""
+    z = lambda *s: torch.zeros(s, dtype=BF16)
+    wide = z(2, 3, 4, 192)
+    rp = dsa.make_rope_params(nt=6, h=4, d=64, dtype=dsa.DTYPE_BF16, x_strides=(768, 192), y_strides=(768, 192))
+    k = z(2, 3, 1, 576)
+    shared = dsa.make_rope_params(nt=6, h=4, x_heads=1, d=64, dtype=dsa.DTYPE_BF16, x_strides=(576, 576))
+    flat = z(2, 3, 300)
+    joined = dsa.make_rope_params(nt=6, h=4, d=64, dtype=dsa.DTYPE_BF16, x_strides=(300, 64))
+    for r, x, y in ((rp, wide[..., 128:], wide[..., :64]), (rp, z(6, 1, 4, 192)[..., 64:128], z(1, 6, 4, 192)[..., :64]),
+                    (shared, k[..., 512:], z(2, 3, 4, 64)), (shared, k[..., 0, 512:], z(2, 3, 256)),
+                    (joined, flat[..., :256], z(6, 4, 64))):
+        rope_call(r, On(x), On(y), False)
+        assert calls.pop()[1][2] == x.data_ptr()
+    for x in (wide[:, :2, :, 128:], wide.transpose(0, 1)[..., 128:], wide[..., 128:].transpose(1, 2), wide[:, ::2, :, :64]):
+        with pytest.raises(dsa.DsaError, match="^x:"):
+            rope_call(rp, On(x), On(wide[..., :64]), False)
+    for x in (z(6, 7, 64), z(2, 3, 7, 64), z(1, 7, 64), z(12, 1, 64)[::2]):     # one head is asked for
+        r = dsa.make_rope_params(nt=x.shape[0], h=4, x_heads=1, d=64, dtype=dsa.DTYPE_BF16)
+        with pytest.raises(dsa.DsaError, match="^x:"):
+            rope_call(r, On(x), On(z(x.shape[0], 4, 64)), False)
+    p, kv, a, keep = prefix_args()
+    for t in (z(2, 16, 1, 576), z(1, 30, 576), z(30, 1, 1, 576), z(3, 10, 600)[..., :576]):
+        stride = t.stride(-3) if t.shape[-2] == 1 else t.stride(-2)
+        dsa.mla_shared_prefix(p, kv, 2, **{**a, "kv_cache": On(t), "kv_row_stride": stride}, stream=0)
+        assert calls.pop()[1][6:8] == (t.data_ptr(), stride)
+    refused("kv_cache", dsa.mla_shared_prefix, p, kv, 2, **{**a, "kv_cache": On(z(2, 16, 2, 576)[:, :, 0]), "kv_row_stride": 576})
+    assert not calls
