@@ -319,8 +319,8 @@ __global__ void __launch_bounds__(kPlanThreads) k17_prefix_plan(const PrefixPara
 //               lane quarter, 64 positions each.  The row maximum is merged
 //               over the four threads of a row; it is raised only past 2^8,
 //               then O is rescaled.  P goes to shared memory in bf16.
-// 64 queries x 128 heads over a shared 32K prefix take 487 us, 1.23 PFLOP/s:
-// 0.73 of the measured bf16 rate, at the chip's power limit.  P as a bf16 pair
+// 64 queries x 128 heads over a shared 32K prefix take 484-499 us, 1.20-1.23
+// PFLOP/s: 0.71-0.73 of the measured bf16 rate, at the chip's power limit.  P as a bf16 pair
 // (hi + lo, as in the sparse attention) took 27% more.  A tile takes about
 // 4900 cycles, its 68 MMAs at least 4760.
 // ---------------------------------------------------------------------------
